@@ -29,6 +29,10 @@ Functions (names as in the C ABI):
   the gradients ``dr, dw, dk, dv, da, db`` and ``d_state_in`` (fp32), given the
   per-position states of the forward pass.
 
+The gated delta rule (``include/gdr.h``; module ``gdr``): ``gdr_forward``, ``gdr_step``.  Draft verification (``include/draft.h``;
+module ``draft``): ``draft_verify`` -> ``(tokens, kept)``, where ``kept`` is what
+``wkv7_state_commit`` takes.
+
 Tensors: r, w, k, v, a, b are [B, T, H, 64] bf16 or fp32 on the GPU; the
 state is [B, H, 64, 64] fp32 with row i a key channel and column j a value
 channel.
@@ -94,6 +98,12 @@ def lib():
         L.wkv7_backward_ckpt.argtypes = [vp] * 6 + [ci] + [vp] * 10 + [ci, ci, ci, ci, vp]
         L.wkv7_backward_ckpt.restype = ci
         L.wkv7_state_reset.restype = ci
+        L.gdr_forward.argtypes = [vp] * 5 + [ci, vp, vp, ci, vp, vp, cf] + [ci] * 6 + [vp]
+        L.gdr_forward.restype = ci
+        L.gdr_step.argtypes = [vp] * 5 + [ci, vp, vp, ci, vp, vp, cf] + [ci] * 6 + [vp]
+        L.gdr_step.restype = ci
+        L.draft_verify.argtypes = [vp, vp, ci] + [vp] * 6 + [ci] * 3 + [vp]
+        L.draft_verify.restype = ci
         L.wkv7_status_string.argtypes = [ci]
         L.wkv7_status_string.restype = ctypes.c_char_p
         L.wkv7_abi_version.argtypes = []
@@ -141,13 +151,24 @@ def _check_inputs(r, w, k, v, a, b):
     return r.shape
 
 
-def _state_arg(state, B, H, N, device, name):
+def _state_arg(state, B, H, N, device, name, V=None):
     if state is None:
         return None
-    if (state.dtype != torch.float32 or tuple(state.shape) != (B, H, N, N) or not state.is_contiguous()
+    V = N if V is None else V
+    if (state.dtype != torch.float32 or tuple(state.shape) != (B, H, N, V) or not state.is_contiguous()
             or state.device != device):
-        raise ValueError(f"{name} must be a contiguous fp32 [{B}, {H}, {N}, {N}] tensor on {device}")
+        raise ValueError(f"{name} must be a contiguous fp32 [{B}, {H}, {N}, {V}] tensor on {device}")
     return state
+
+
+def _blocks64(H, K, V):
+    """(H, N) by which the commit and the reset, which only move states, take H states of K x V
+    floats: blocks of 64 x 64.  Other sizes go to the C ABI as they are, which refuses them."""
+    if K in (64, 128) and V % 64 == 0:
+        return H * (K * V // 4096), HEAD_SIZE
+    if K != V:
+        raise ValueError(f"states of {K} x {V} are not supported")
+    return H, K
 
 
 def _out_arg(x, shape, device, name, dtypes=(torch.float32, torch.bfloat16)):
@@ -310,21 +331,22 @@ def wkv7_tmix_tail(o, r, k, v, g, r_k, ln_w, ln_b, eps, *, x_dtype=torch.float32
 def wkv7_state_commit(state_pos, accepted, state_in=None, *, state_out=None):
     """State after each row's accepted prefix of a verify step.  Returns state_out.
 
-    state_pos: [B, T, H, N, N] from wkv7_step(per_position=True); accepted: [B]
-    integers.  Row b becomes state_pos[b, accepted[b] - 1], or state_in[b] (zeros
+    state_pos: [B, T, H, N, N] from wkv7_step(per_position=True), or [B, T, H, K, V] from
+    gdr_step(per_position=True); accepted: [B] integers.  Row b becomes state_pos[b, accepted[b] - 1], or state_in[b] (zeros
     when None) for accepted[b] == 0; rows with accepted[b] outside [0, T] keep
     state_out (pass state_out=state_in to commit in place).
     """
     if state_pos.dim() != 5 or not state_pos.is_cuda or state_pos.dtype != torch.float32 \
             or not state_pos.is_contiguous():
         raise ValueError("state_pos must be a contiguous fp32 [B, T, H, N, N] GPU tensor")
-    B, T, H, N, _ = state_pos.shape
+    B, T, H, N, V = state_pos.shape
     dev = state_pos.device
     accepted = _int_rows(accepted, B, dev, "accepted")
-    state_in = _state_arg(state_in, B, H, N, dev, "state_in")
+    state_in = _state_arg(state_in, B, H, N, dev, "state_in", V)
     if state_out is None:
-        state_out = torch.empty((B, H, N, N), dtype=torch.float32, device=dev)
-    _state_arg(state_out, B, H, N, dev, "state_out")
+        state_out = torch.empty((B, H, N, V), dtype=torch.float32, device=dev)
+    _state_arg(state_out, B, H, N, dev, "state_out", V)
+    H, N = _blocks64(H, N, V)
     _check(lib().wkv7_state_commit(_ptr(state_pos), _ptr(accepted), _ptr(state_in), _ptr(state_out),
                                    B, T, H, N, _stream(dev)))
     return state_out
@@ -414,10 +436,12 @@ def wkv7_backward_ckpt(r, w, k, v, a, b, ckpt, d_o, d_state_out=None, *, grads=N
 
 
 def wkv7_state_reset(state, row_mask=None):
-    """Zero state [B, H, 64, 64] in place; with row_mask ([B] bool/uint8) only the flagged rows."""
+    """Zero state [B, H, 64, 64] (or [B, H, K, V] of gdr) in place; with row_mask ([B] bool/uint8)
+    only the flagged rows."""
     if state.dim() != 4 or not state.is_cuda or state.dtype != torch.float32 or not state.is_contiguous():
         raise ValueError("state must be a contiguous fp32 [B, H, N, N] GPU tensor")
-    B, H, N, _ = state.shape
+    B = state.shape[0]
+    H, N = _blocks64(*state.shape[1:])
     if row_mask is not None:
         row_mask = row_mask.to(device=state.device, dtype=torch.uint8).contiguous()
         if row_mask.shape != (B,):
@@ -428,3 +452,7 @@ def wkv7_state_reset(state, row_mask=None):
 
 def abi_version() -> int:
     return int(lib().wkv7_abi_version())
+
+
+from .draft import draft_verify  # noqa: E402
+from .gdr import gdr_forward, gdr_step  # noqa: E402

@@ -4,12 +4,15 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB_PATH = os.path.join(PKG, "libwkv7.so")
-SOURCES = ["wkv7_api.hip", "wkv7_step.hip", "wkv7_chunk.hip", "wkv7_tail.hip", "wkv7_bwd.hip", "wkv7_bwdc.hip"]
+SOURCES = ["wkv7_api.hip", "wkv7_step.hip", "wkv7_chunk.hip", "wkv7_tail.hip", "wkv7_bwd.hip", "wkv7_bwdc.hip",
+           "gdr_api.hip", "gdr_step.hip", "draft.hip"]
 ARCH = "gfx950"
 
 # -packed-fp32-ops: no packed fp32 math is emitted for any kernel of this library.
@@ -24,10 +27,21 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
-    """Compile every source into libwkv7.so.  Always recompiles.  Returns the path."""
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
+    """Compile every source (a process each) and link libwkv7.so.  Always recompiles.  Returns the path."""
+    flags = [hipcc()] + HIPCC_FLAGS + (extra_flags or []) + ["-I", os.path.join(ROOT, "include")]
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [hipcc()] + HIPCC_FLAGS + (extra_flags or []) + ["-I", os.path.join(ROOT, "include")] + srcs + ["-o", tmp]
+    with tempfile.TemporaryDirectory() as work:
+        objs = [os.path.join(work, s + ".o") for s in SOURCES]
+        cmds = [[f for f in flags if f != "-shared"] + ["-c", os.path.join(CSRC, s), "-o", o]
+                for s, o in zip(SOURCES, objs)]
+        with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            list(pool.map(lambda c: _run(c, verbose), cmds))
+        _run([hipcc(), "-shared", f"--offload-arch={ARCH}"] + objs + ["-o", tmp], verbose)
+    os.replace(tmp, LIB_PATH)
+    return LIB_PATH
+
+
+def _run(cmd: list[str], verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -38,8 +52,6 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
         raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
     if verbose and err.strip():
         print(err, file=sys.stderr)
-    os.replace(tmp, LIB_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":

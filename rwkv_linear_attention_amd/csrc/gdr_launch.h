@@ -1,0 +1,34 @@
+// gdr_launch.h -- internal launch entry points of the gated delta rule and of draft
+// verification.  Arguments are validated by gdr_api.hip before these run.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+namespace gdr {
+
+struct SeqArgs {
+    const void *q, *k, *v;     // [B,T,Hk,K], [B,T,Hk,K], [B,T,H,V], in_dtype
+    const float *g, *beta;     // [B,T,H]
+    const float *state_in;     // [B,H,K,V] or nullptr (zeros)
+    void *o;                   // [B,T,H,V], o_dtype
+    float *state_out;          // [B,H,K,V] or nullptr (step with state_pos)
+    float *state_pos;          // [B,T,H,K,V] or nullptr
+    const int *lengths;        // [B] or nullptr
+    float scale;
+    int B, T, Hk, H, K, V;
+    int in_bf16, o_bf16;
+};
+
+struct DraftArgs {
+    const void *target, *draft;
+    const int *tokens, *n_draft;
+    const float *u, *u_draw;
+    int *out, *kept;
+    int B, N, vocab;
+    int bf16;
+};
+
+hipError_t launch_step(const SeqArgs &a, hipStream_t stream);
+hipError_t launch_draft(const DraftArgs &a, hipStream_t stream);
+
+}  // namespace gdr

@@ -1,0 +1,223 @@
+"""GPU parity of the gated delta rule (gdr_forward, gdr_step) with the fp64 oracle.
+
+Tolerances (relative L2; see parity.py for the per-head and per-element bounds).  An fp32
+result is a sum of products in fp32 (2^-24 each way) in which some operands were split into
+two bf16 pieces: a piece rounds to half a step (2^-9 relative), two leave at most 2^-18 =
+3.8e-6 and 7e-7 in the root mean square.  At most three such operands stand between an
+input and an output (the state, the residual and the triangular inverse), 3 x 7e-7 = 2.1e-6,
+and the rule does not amplify an error (unit keys, beta <= 1, decay <= 1).  4e-6 leaves the
+accumulation of the sums as much again.  A bf16 output adds half a step, 2^-8 relative.
+"""
+import numpy as np
+import pytest
+import torch
+
+from gdr_inputs import DT, NAMES, make, on_gpu
+from oracle import gdr
+from parity import HEADS_SEQ, HEADS_STATE, check
+
+pytestmark = pytest.mark.gpu
+
+TOL = 4e-6
+BF16 = 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import rwkv_linear_attention_amd as m
+    m.lib()
+    return m
+
+
+def check_o(o, ref, what):
+    bf16 = o.dtype == torch.bfloat16
+    check(o, ref, TOL + (BF16 if bf16 else 0.0), what, HEADS_SEQ, BF16 if bf16 else 0.0)
+
+
+# B, T, Hk, H, K, V, input, output
+SHAPES = [(1, 1, 1, 1, 64, 64, "bf16", "fp32"), (2, 5, 2, 4, 64, 64, "bf16", "bf16"),
+          (1, 8, 1, 3, 128, 64, "bf16", "fp32"), (2, 9, 2, 2, 64, 128, "fp32", "fp32"),
+          (1, 31, 1, 2, 128, 128, "bf16", "fp32"), (2, 32, 1, 1, 128, 192, "bf16", "bf16"),
+          (1, 33, 3, 3, 64, 64, "fp32", "bf16"), (3, 64, 2, 6, 64, 64, "bf16", "fp32"),
+          (1, 65, 1, 1, 128, 512, "bf16", "fp32"), (1, 100, 2, 2, 128, 128, "fp32", "fp32"),
+          (2, 257, 1, 2, 64, 128, "bf16", "fp32"), (1, 700, 2, 2, 128, 64, "bf16", "fp32")]
+
+
+@pytest.mark.parametrize("B,T,Hk,H,K,V,dtype,out", SHAPES)
+@pytest.mark.parametrize("entry", ["forward", "step"])
+def test_against_the_oracle(lib, entry, B, T, Hk, H, K, V, dtype, out):
+    inp = make(B, T, Hk, H, K, V, seed=T + H, dtype=dtype)
+    ref_o, ref_s, _ = gdr.forward(*(inp[n] for n in NAMES), inp["state"], K ** -0.5)
+    d = on_gpu(inp)
+    run = lib.gdr_forward if entry == "forward" else lib.gdr_step
+    o, s = run(*(d[n] for n in NAMES), d["state"], o_dtype=DT[out])
+    assert o.dtype == DT[out]
+    check_o(o, ref_o, "o")
+    check(s, ref_s, TOL, "state", HEADS_STATE)
+
+
+@pytest.mark.parametrize("T", [3, 40])
+@pytest.mark.parametrize("entry", ["forward", "step"])
+def test_without_a_state_in_place_and_with_a_scale(lib, entry, T):
+    inp = make(2, T, 1, 2, 64, 64, seed=5, state=False)
+    d = on_gpu(inp)
+    run = lib.gdr_forward if entry == "forward" else lib.gdr_step
+    args = [d[n] for n in NAMES]
+    ref_o, ref_s, _ = gdr.forward(*(inp[n] for n in NAMES), None, 2.5)
+    o, s = run(*args, scale=2.5)
+    check_o(o, ref_o, "o")
+    check(s, ref_s, TOL, "state", HEADS_STATE)
+    first = s.clone()
+    o2, s2 = run(*args, s, scale=2.5, state_out=s)     # on from there, in place
+    assert s2 is s
+    ref_o2, ref_s2, _ = gdr.forward(*(inp[n] for n in NAMES), first, 2.5)
+    check_o(o2, ref_o2, "o in place")
+    check(s, ref_s2, TOL, "state in place", HEADS_STATE)
+
+
+@pytest.mark.parametrize("T,lengths", [(7, [0, 7, 3, 1]), (90, [90, 0, 1, 64]), (90, [32, 33, 31, 200]),
+                                       (70, [-3, 9, 8, 69])])
+def test_lengths(lib, T, lengths):
+    inp = make(4, T, 1, 2, 128, 64, seed=T, dtype="bf16")
+    ref_o, ref_s, _ = gdr.forward(*(inp[n] for n in NAMES), inp["state"], 128 ** -0.5, lengths)
+    for n in NAMES:   # what stands behind a row's end is not used
+        for b, L in enumerate(lengths):
+            inp[n][b, max(0, min(L, T)):] = float("nan")
+    d = on_gpu(inp)
+    o = torch.full((4, T, 2, 64), 7.0, device="cuda")
+    o, s = lib.gdr_forward(*(d[n] for n in NAMES), d["state"], o=o, lengths=torch.tensor(lengths))
+    for b, L in enumerate(lengths):
+        L = max(0, min(L, T))
+        assert bool((o[b, L:] == 7.0).all())
+        if L:
+            check_o(o[b:b + 1, :L], ref_o[b:b + 1, :L], f"o of row {b}")
+        else:
+            assert torch.equal(s[b], d["state"][b])
+    check(s, ref_s, TOL, "state", HEADS_STATE)
+
+
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 128)])
+def test_verify_commit_chain(lib, K, V):
+    """Serving as it is used: prefill, a verify step over drafts, the drafts judged, the states committed, on."""
+    B, H, Hk, N, vocab = 3, 4, 2, 4, 1000
+    pre, ver, nxt = (make(B, T, Hk, H, K, V, seed=T, dtype="bf16") for T in (50, N + 1, 1))
+    ref = {n: gdr.as_f64(x) for n, x in ver.items()}
+    dp, dv, dn = on_gpu(pre), on_gpu(ver), on_gpu(nxt)
+    _, s0 = lib.gdr_forward(*(dp[n] for n in NAMES), dp["state"])
+    o, none, pos = lib.gdr_step(*(dv[n] for n in NAMES), s0, per_position=True, write_state_out=False)
+    assert none is None
+    gen = torch.Generator().manual_seed(1)
+    target = torch.softmax(2 * torch.randn(B, N + 1, vocab, generator=gen), -1).cuda()
+    tokens = torch.randint(0, vocab, (B, N), generator=gen, dtype=torch.int32).cuda()
+    u = torch.full((B, N), 0.0, device="cuda")
+    u[1, 2], u[2, 0] = 1.0, 1.0     # row 1 keeps two drafts, row 2 none (a sure drafter)
+    out, kept = lib.draft_verify(target, tokens, u, torch.rand(B, generator=gen).cuda())
+    assert kept.tolist() == [N + 1, 3, 1]
+    s1 = lib.wkv7_state_commit(pos, kept, s0, state_out=s0.clone())
+    _, ref_s0, _ = gdr.forward(*(pre[n] for n in NAMES), pre["state"], K ** -0.5)
+    ref_o, _, ref_pos = gdr.forward(*(ref[n] for n in NAMES), ref_s0, K ** -0.5)
+    check_o(o, ref_o, "o of the verify step")
+    want = np.stack([ref_pos[b, n - 1] for b, n in enumerate(kept.tolist())])
+    check(s1, want, TOL, "committed state", HEADS_STATE)
+    o2, s2 = lib.gdr_step(*(dn[n] for n in NAMES), s1, state_out=s1)
+    ref_o2, ref_s2, _ = gdr.forward(*(nxt[n] for n in NAMES), want, K ** -0.5)
+    check_o(o2, ref_o2, "o of the next token")
+    check(s2, ref_s2, TOL, "state of the next token", HEADS_STATE)
+    lib.wkv7_state_reset(s2, torch.tensor([True, False, True]))
+    assert not s2[0].any() and not s2[2].any() and bool(s2[1].any())
+
+
+@pytest.mark.parametrize("T", [4, 80])
+def test_dropped_states_and_idle_gates(lib, T):
+    """g = -inf drops the state before a token, beta = 0 writes nothing, beta = 1 with a unit key replaces."""
+    inp = make(2, T, 1, 2, 64, 64, seed=11, dtype="fp32")
+    inp["g"][0, T // 2] = float("-inf")
+    inp["g"][1, 0] = -200.0
+    inp["beta"][0, 1] = 0.0
+    inp["beta"][1] = 1.0
+    ref_o, ref_s, _ = gdr.forward(*(inp[n] for n in NAMES), inp["state"], 1.0)
+    d = on_gpu(inp)
+    for run in (lib.gdr_forward, lib.gdr_step):
+        o, s = run(*(d[n] for n in NAMES), d["state"], scale=1.0)
+        check_o(o, ref_o, "o")
+        check(s, ref_s, TOL, "state", HEADS_STATE)
+
+
+@pytest.mark.parametrize("decay", [0.0, 1.0, 30.0])
+def test_one_key_over_and_over(lib, decay):
+    """Equal keys make the chunk's triangular system as far from the identity as it gets."""
+    inp = make(1, 96, 1, 1, 128, 64, seed=2, dtype="bf16", decay=decay)
+    inp["k"][:] = inp["k"][:, :1]
+    ref_o, ref_s, _ = gdr.forward(*(inp[n] for n in NAMES), inp["state"], 1.0)
+    d = on_gpu(inp)
+    for run in (lib.gdr_forward, lib.gdr_step):
+        o, s = run(*(d[n] for n in NAMES), d["state"], scale=1.0)
+        check_o(o, ref_o, "o")
+        check(s, ref_s, TOL, "state", HEADS_STATE)
+
+
+@pytest.mark.parametrize("T", [3, 70])
+def test_value_columns_are_apart(lib, T):
+    """A NaN in one value channel stays in its column (and, chunked, within its chunk before the token)."""
+    inp = make(1, T, 1, 1, 64, 64, seed=6, dtype="fp32")
+    d = on_gpu(inp)
+    o1, s1 = lib.gdr_forward(*(d[n] for n in NAMES), d["state"])
+    at = T // 2 + 5 if T > 9 else 1
+    d["v"][0, at, 0, 7] = float("nan")
+    o2, s2 = lib.gdr_forward(*(d[n] for n in NAMES), d["state"])
+    cols = torch.arange(64, device="cuda") != 7
+    assert torch.equal(o1[..., cols], o2[..., cols]) and torch.equal(s1[..., cols], s2[..., cols])
+    assert bool(o2[0, at:, 0, 7].isnan().all()) and bool(s2[0, 0, :, 7].isnan().all())
+    chunk = at // 32 * 32 if T >= 9 else at
+    assert not bool(o2[0, :chunk, 0, 7].isnan().any())
+
+
+def test_streams_and_graph_replays(lib):
+    """On a side stream, and captured: every replay on new inputs against the eager result."""
+    shape = (2, 40, 1, 2, 64, 64)
+    ins = [on_gpu(make(*shape, seed=s)) for s in range(3)]
+    eager = [lib.gdr_forward(*(d[n] for n in NAMES), d["state"]) for d in ins]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        o, s = lib.gdr_forward(*(ins[1][n] for n in NAMES), ins[1]["state"])
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(o, eager[1][0]) and torch.equal(s, eager[1][1])
+    static = {n: x.clone() for n, x in ins[0].items()}
+    o, s = torch.empty_like(eager[0][0]), torch.empty_like(eager[0][1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lib.gdr_forward(*(static[n] for n in NAMES), static["state"], o=o, state_out=s)
+    for i in (1, 2, 0, 1):
+        for n, x in static.items():
+            x.copy_(ins[i][n])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, eager[i][0]) and torch.equal(s, eager[i][1])
+        again = lib.gdr_forward(*(ins[i][n] for n in NAMES), ins[i]["state"])
+        assert torch.equal(again[0], o)
+
+
+def test_refusals(lib):
+    d = on_gpu(make(2, 12, 2, 4, 64, 64))
+    args = [d[n] for n in NAMES]
+    with pytest.raises(ValueError):
+        lib.gdr_forward(*args[:2], args[2].transpose(1, 2), *args[3:])
+    with pytest.raises(ValueError):
+        lib.gdr_forward(args[0], args[1][:, :, :1].contiguous(), *args[2:])
+    with pytest.raises(ValueError):
+        lib.gdr_forward(*args[:3], args[3].double(), args[4])
+    with pytest.raises(TypeError):
+        lib.gdr_forward(args[0].half(), args[1].half(), args[2].half(), *args[3:])
+    with pytest.raises(ValueError):
+        lib.gdr_forward(*args, d["state"][:, :, :32].contiguous())
+    with pytest.raises(ValueError):
+        lib.gdr_step(*args, o=torch.empty(2, 12, 4, 32, device="cuda"))
+    with pytest.raises(ValueError):
+        lib.gdr_step(*args, write_state_out=False)
+    with pytest.raises(lib.Wkv7Error):   # 96 channels
+        x = on_gpu(make(1, 4, 1, 1, 96, 64))
+        lib.gdr_forward(*(x[n] for n in NAMES), x["state"])
+    with pytest.raises(lib.Wkv7Error):   # o on top of v
+        y = on_gpu(make(2, 12, 2, 4, 64, 64, dtype="fp32"))
+        lib.gdr_forward(*(y[n] for n in NAMES), o=y["v"])
