@@ -24,6 +24,7 @@
  *   o                   : [B, T, H, V]      of o_dtype
  *   state_in, state_out : [B, H, K, V]      fp32
  *   state_pos           : [B, T, H, K, V]   fp32, [b,t,h] = S after token t
+ *   ckpt, work          : [B, ceil(T/64), H, K*V] fp32, opaque
  * K is 64 or 128; V is a multiple of 64 up to GDR_MAX_V; Hk divides H.
  * in_dtype and o_dtype are WKV7_F32 or WKV7_BF16.
  *
@@ -36,10 +37,11 @@
  * K V / 4096 consecutive blocks of 64 x 64 floats, so pass H * K * V / 4096 as
  * their H (and 64 as N).
  *
- * NUMERICS.  The state and every accumulation are fp32.  Value channels stay
- * independent: a NaN or Inf in v[b,t,h,j] reaches only column j of that head, from
- * token t on, except that gdr_forward forms the outputs of 32 tokens together, so
- * there it can also reach the earlier tokens of the same 32-token chunk.
+ * NUMERICS.  The state and every accumulation are fp32.  Results match
+ * an fp64 evaluation to a relative L2 error below 1e-6 (plus the rounding of a bf16 o).
+ * Value channels stay independent: a NaN or Inf in v[b,t,h,j] reaches only column j of
+ * that head, from token t on, except that gdr_forward forms the outputs of 32 tokens
+ * together, so there it can also reach the earlier tokens of the same 32-token chunk.
  */
 #ifndef GDR_H
 #define GDR_H
@@ -50,9 +52,14 @@
 extern "C" {
 #endif
 
-/* Limits (WKV7_ERR_SHAPE beyond them): V <= GDR_MAX_V; B * H * V <= GDR_MAX_COLUMNS
- * (a launch holds fewer than 2^32 threads).  Tensor offsets are 64-bit. */
+/* Limits (WKV7_ERR_SHAPE beyond them): V <= GDR_MAX_V; T <= GDR_MAX_T; H * V <= GDR_MAX_ROW (a chunk's
+ * rows are addressed with 32-bit offsets from its first); B * H * V <= GDR_MAX_COLUMNS and
+ * B * ceil(T/64) * H <= GDR_MAX_BLOCKS (a launch holds fewer than 2^32 threads; the latter
+ * for the training pair).  Tensor offsets are 64-bit. */
 #define GDR_MAX_V 512
+#define GDR_MAX_ROW 16777216
+#define GDR_MAX_T 1073741824
+#define GDR_MAX_BLOCKS 8388608
 #define GDR_MAX_COLUMNS 268435456
 
 /*
@@ -81,6 +88,36 @@ int gdr_forward(const void *q, const void *k, const void *v, const float *g, con
 int gdr_step(const void *q, const void *k, const void *v, const float *g, const float *beta, int in_dtype,
              const float *state_in, void *o, int o_dtype, float *state_out, float *state_pos, float scale,
              int B, int T, int Hk, int H, int K, int V, void *stream);
+
+/*
+ * gdr_forward_ckpt -- the forward pass of training: gdr_forward (fp32 o, every row T
+ * tokens) that also keeps what gdr_backward_ckpt reads.
+ *
+ *   ckpt  : the state entering every 64 tokens, [B, ceil(T/64), H, K*V] fp32.
+ *   resid : the residuals R of every token, [B, T, H, V] fp32.
+ * Both may be NULL only when T = 0.
+ */
+int gdr_forward_ckpt(const void *q, const void *k, const void *v, const float *g, const float *beta, int in_dtype,
+                     const float *state_in, float *o, float *state_out, float *ckpt, float *resid, float scale,
+                     int B, int T, int Hk, int H, int K, int V, void *stream);
+
+/*
+ * gdr_backward_ckpt -- the gradients, given what gdr_forward_ckpt kept from the same
+ * inputs.  For a loss L with dL/do = d_o and dL/dS_T = d_state_out:
+ *
+ *   d_o         : [B,T,H,V] fp32.
+ *   d_state_out : [B,H,K,V] fp32, or NULL (zeros).
+ *   dq, dk      : [B,T,Hk,K] fp32, summed over the value heads of a group in a fixed
+ *                 order (no atomics: the same call gives the same bits).
+ *   dv          : [B,T,H,V] fp32.     dg, dbeta : [B,T,H] fp32.
+ *   d_state_in  : [B,H,K,V] fp32; may equal d_state_out.
+ *   work        : scratch of ckpt's size; what it holds afterwards is unspecified.
+ * v itself is not read (resid stands for it).  With T = 0 only d_state_in is written.
+ */
+int gdr_backward_ckpt(const void *q, const void *k, const float *g, const float *beta, int in_dtype,
+                      const float *ckpt, const float *resid, const float *d_o, const float *d_state_out,
+                      float *dq, float *dk, float *dv, float *dg, float *dbeta, float *d_state_in, float *work,
+                      float scale, int B, int T, int Hk, int H, int K, int V, void *stream);
 
 #ifdef __cplusplus
 }

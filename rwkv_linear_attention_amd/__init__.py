@@ -29,7 +29,8 @@ Functions (names as in the C ABI):
   the gradients ``dr, dw, dk, dv, da, db`` and ``d_state_in`` (fp32), given the
   per-position states of the forward pass.
 
-The gated delta rule (``include/gdr.h``; module ``gdr``): ``gdr_forward``, ``gdr_step``.  Draft verification (``include/draft.h``;
+The gated delta rule (``include/gdr.h``; module ``gdr``): ``gdr_forward``, ``gdr_step``,
+``gdr_forward_ckpt`` and ``gdr_backward_ckpt``.  Draft verification (``include/draft.h``;
 module ``draft``): ``draft_verify`` -> ``(tokens, kept)``, where ``kept`` is what
 ``wkv7_state_commit`` takes.
 
@@ -102,6 +103,10 @@ def lib():
         L.gdr_forward.restype = ci
         L.gdr_step.argtypes = [vp] * 5 + [ci, vp, vp, ci, vp, vp, cf] + [ci] * 6 + [vp]
         L.gdr_step.restype = ci
+        L.gdr_forward_ckpt.argtypes = [vp] * 5 + [ci] + [vp] * 5 + [cf] + [ci] * 6 + [vp]
+        L.gdr_forward_ckpt.restype = ci
+        L.gdr_backward_ckpt.argtypes = [vp] * 4 + [ci] + [vp] * 11 + [cf] + [ci] * 6 + [vp]
+        L.gdr_backward_ckpt.restype = ci
         L.draft_verify.argtypes = [vp, vp, ci] + [vp] * 6 + [ci] * 3 + [vp]
         L.draft_verify.restype = ci
         L.wkv7_status_string.argtypes = [ci]
@@ -455,4 +460,4 @@ def abi_version() -> int:
 
 
 from .draft import draft_verify  # noqa: E402
-from .gdr import gdr_forward, gdr_step  # noqa: E402
+from .gdr import gdr_backward_ckpt, gdr_forward, gdr_forward_ckpt, gdr_step  # noqa: E402

@@ -12,7 +12,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB_PATH = os.path.join(PKG, "libwkv7.so")
 SOURCES = ["wkv7_api.hip", "wkv7_step.hip", "wkv7_chunk.hip", "wkv7_tail.hip", "wkv7_bwd.hip", "wkv7_bwdc.hip",
-           "gdr_api.hip", "gdr_step.hip", "draft.hip"]
+           "gdr_api.hip", "gdr_step.hip", "gdr_chain.hip", "gdr_grad.hip", "draft.hip"]
 ARCH = "gfx950"
 
 # -packed-fp32-ops: no packed fp32 math is emitted for any kernel of this library.

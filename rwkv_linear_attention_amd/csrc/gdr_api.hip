@@ -13,7 +13,11 @@
 
 namespace {
 
+// Sequences shorter than this go to the step kernel in gdr_forward.
+constexpr int kChainMinT = 9;
+
 static_assert(GDR_MAX_COLUMNS / 64 * 512ll < (1ll << 32) && GDR_MAX_COLUMNS / 32 * 64ll < (1ll << 32) &&
+                  GDR_MAX_BLOCKS * 256ll < (1ll << 32) &&
                   DRAFT_MAX_ROWS * 1024ll < (1ll << 32),
               "a launch must hold fewer than 2^32 threads");
 
@@ -59,7 +63,7 @@ int check_shape(int B, int T, int Hk, int H, int K, int V)
     if (B < 1 || T < 0 || Hk < 1 || H < 1 || H % Hk != 0 || V > GDR_MAX_V)
         return WKV7_ERR_SHAPE;
     const int64_t heads = static_cast<int64_t>(B) * H;
-    if (heads > GDR_MAX_COLUMNS / V)
+    if (T > GDR_MAX_T || H > GDR_MAX_ROW / V || heads > GDR_MAX_COLUMNS / V)
         return WKV7_ERR_SHAPE;
     // B T H K V 4 bytes (the per-position states, the largest buffer) within int64
     if (T > 0 && heads > INT64_MAX / (static_cast<int64_t>(K) * V * 8) / T)
@@ -67,8 +71,15 @@ int check_shape(int B, int T, int Hk, int H, int K, int V)
     return WKV7_OK;
 }
 
+// The training pair's blocks of 64 tokens.
+bool blocks_ok(int B, int T, int H)
+{
+    const int64_t blocks = (static_cast<int64_t>(T) + gdr::kBlock - 1) / gdr::kBlock;
+    return blocks == 0 || static_cast<int64_t>(B) * H <= GDR_MAX_BLOCKS / blocks;
+}
+
 struct Sizes {
-    int64_t qk, v, gate, state;  // elements
+    int64_t qk, v, gate, state, ckpt;  // elements
     Sizes(int B, int T, int Hk, int H, int K, int V)
     {
         const int64_t tok = static_cast<int64_t>(B) * T;
@@ -76,16 +87,19 @@ struct Sizes {
         v = tok * H * V;
         gate = tok * H;
         state = static_cast<int64_t>(B) * H * K * V;
+        ckpt = static_cast<int64_t>((static_cast<int64_t>(T) + gdr::kBlock - 1) / gdr::kBlock) * state;
     }
 };
 
-int check_seq(const gdr::SeqArgs &a, int in_dtype, int o_dtype, bool out_optional)
+int check_seq(const gdr::SeqArgs &a, int in_dtype, int o_dtype, bool out_optional, bool training = false)
 {
     if (!is_dtype(in_dtype) || !is_dtype(o_dtype))
         return WKV7_ERR_UNSUPPORTED;
     const int st = check_shape(a.B, a.T, a.Hk, a.H, a.K, a.V);
     if (st != WKV7_OK)
         return st;
+    if (training && !blocks_ok(a.B, a.T, a.H))
+        return WKV7_ERR_SHAPE;
     if (!a.state_out && !(out_optional && a.state_pos && a.T > 0))
         return WKV7_ERR_NULL;
     if (a.T > 0 && (!a.q || !a.k || !a.v || !a.g || !a.beta || !a.o))
@@ -104,6 +118,8 @@ int check_seq(const gdr::SeqArgs &a, int in_dtype, int o_dtype, bool out_optiona
     bufs.out(a.o, n.v * elem(o_dtype));
     bufs.out(a.state_out, n.state * 4);
     bufs.out(a.state_pos, a.T > 0 ? n.state * a.T * 4 : 0);
+    bufs.out(a.ckpt, n.ckpt * 4);
+    bufs.out(a.resid, n.v * 4);
     return bufs.check();
 }
 
@@ -145,7 +161,7 @@ int gdr_forward(const void *q, const void *k, const void *v, const float *g, con
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (T == 0)
         return pass_through(state_in, state_out, Sizes(B, T, Hk, H, K, V).state, s);
-    return done(gdr::launch_step(a, s));
+    return done(T < kChainMinT ? gdr::launch_step(a, s) : gdr::launch_chain(a, s));
 }
 
 int gdr_step(const void *q, const void *k, const void *v, const float *g, const float *beta, int in_dtype,
@@ -161,6 +177,74 @@ int gdr_step(const void *q, const void *k, const void *v, const float *g, const 
     if (T == 0)
         return pass_through(state_in, state_out, Sizes(B, T, Hk, H, K, V).state, s);
     return done(gdr::launch_step(a, s));
+}
+
+int gdr_forward_ckpt(const void *q, const void *k, const void *v, const float *g, const float *beta, int in_dtype,
+                     const float *state_in, float *o, float *state_out, float *ckpt, float *resid, float scale,
+                     int B, int T, int Hk, int H, int K, int V, void *stream)
+{
+    gdr::SeqArgs a = make_args(q, k, v, g, beta, in_dtype, state_in, o, WKV7_F32, state_out, scale, B, T, Hk, H, K, V);
+    a.ckpt = ckpt;
+    a.resid = resid;
+    const int st = check_seq(a, in_dtype, WKV7_F32, false, true);
+    if (st != WKV7_OK)
+        return st;
+    if (T > 0 && (!ckpt || !resid))
+        return WKV7_ERR_NULL;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (T == 0)
+        return pass_through(state_in, state_out, Sizes(B, T, Hk, H, K, V).state, s);
+    return done(gdr::launch_chain(a, s));
+}
+
+int gdr_backward_ckpt(const void *q, const void *k, const float *g, const float *beta, int in_dtype,
+                      const float *ckpt, const float *resid, const float *d_o, const float *d_state_out,
+                      float *dq, float *dk, float *dv, float *dg, float *dbeta, float *d_state_in, float *work,
+                      float scale, int B, int T, int Hk, int H, int K, int V, void *stream)
+{
+    if (!is_dtype(in_dtype))
+        return WKV7_ERR_UNSUPPORTED;
+    int st = check_shape(B, T, Hk, H, K, V);
+    if (st != WKV7_OK)
+        return st;
+    if (!blocks_ok(B, T, H))
+        return WKV7_ERR_SHAPE;
+    if (!d_state_in)
+        return WKV7_ERR_NULL;
+    if (T > 0 && (!q || !k || !g || !beta || !ckpt || !resid || !d_o || !dq || !dk || !dv || !dg || !dbeta || !work))
+        return WKV7_ERR_NULL;
+    const Sizes n(B, T, Hk, H, K, V);
+    Buffers bufs;
+    bufs.in(q, n.qk * elem(in_dtype));
+    bufs.in(k, n.qk * elem(in_dtype));
+    bufs.in(g, n.gate * 4);
+    bufs.in(beta, n.gate * 4);
+    bufs.in(ckpt, n.ckpt * 4);
+    bufs.in(resid, n.v * 4);
+    bufs.in(d_o, n.v * 4);
+    if (d_state_out != d_state_in)
+        bufs.in(d_state_out, n.state * 4);
+    bufs.out(dq, n.qk * 4);
+    bufs.out(dk, n.qk * 4);
+    bufs.out(dv, n.v * 4);
+    bufs.out(dg, n.gate * 4);
+    bufs.out(dbeta, n.gate * 4);
+    bufs.out(d_state_in, n.state * 4);
+    bufs.out(work, n.ckpt * 4);
+    st = bufs.check();
+    if (st != WKV7_OK)
+        return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (T == 0)
+        return pass_through(d_state_out, d_state_in, n.state, s);
+    gdr::BwdArgs a = {};
+    a.q = q; a.k = k; a.g = g; a.beta = beta; a.ckpt = ckpt; a.resid = resid; a.d_o = d_o;
+    a.d_state_out = d_state_out;
+    a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.d_state_in = d_state_in; a.work = work;
+    a.scale = scale;
+    a.B = B; a.T = T; a.Hk = Hk; a.H = H; a.K = K; a.V = V;
+    a.in_bf16 = in_dtype == WKV7_BF16;
+    return done(gdr::launch_backward(a, s));
 }
 
 int draft_verify(const void *target, const void *draft, int dtype, const int *tokens, const int *n_draft,

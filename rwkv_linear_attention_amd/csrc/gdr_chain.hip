@@ -1,0 +1,806 @@
+// gdr_chain.hip -- the gated delta rule over whole sequences, chunk by chunk on the matrix
+// cores: the parallel forward pass, and the backward pass's walk of the state's gradient.
+//
+// CHUNK FORM.  Over a chunk of C = 32 tokens entered by state S, with alpha_i = exp(g_i),
+// P_ij = alpha_{j+1} .. alpha_i, gamma_i = alpha_first .. alpha_i and gamma_C its last,
+//     Z  = V - diag(gamma) K S                      the residuals if the chunk wrote nothing
+//     R  = (I + X B)^-1 Z,     X_ij = P_ij k_i.k_j for j < i, B = diag(beta)
+//     O  = scale diag(gamma) Q S + A R,  A_ij = scale P_ij q_i.k_j beta_j for j <= i
+//     S' = gamma_C S + K^T diag(beta_j P_Cj) R.
+// Backward, from the gradient G of the state behind the chunk (dO the gradient of O):
+//     D  = A'^T dO + diag(P_C) K G,                 A' = A without beta
+//     Y  = (I + B X)^-T D                           (Y is the gradient of beta R; dV = beta Y)
+//     G' = gamma_C G + Q^T diag(scale gamma) dO - K^T diag(gamma beta) Y.
+// Both walks have the same shape: two products with the state, a triangular 32 x 32
+// product, and an update of the state; value columns never meet.  The decays enter as
+// products of alphas (a column of P per lane), so no exponent range limits them and
+// alpha = 0 is exact.
+//
+// MAPPING.  A workgroup takes 64 value columns of one head and walks its chunks in order,
+// with one barrier per chunk.  Four consumer waves keep 16 columns of the state each, in
+// the accumulator layout of the matrix cores, and do the products above; four producer
+// waves prepare what does not depend on the state, up to three chunks ahead:
+//     decay wave  (s + 3)  P, gamma and the vectors derived from them
+//     K wave      (s + 2)  X = P o K K^T;  the rows of K to LDS one chunk later
+//     Q wave      (s + 2)  A = P o Q K^T;  A and the rows of Q to LDS one chunk later
+//     inverse     (s + 1)  (I + X B)^-1 - I: two 16 x 16 blocks by substitution in fp32,
+//                          the block below by fp32 matrix products.
+// (Substitution, not products of powers of X: with equal keys the powers grow to 3000 and
+// cancel.)  A row of K serves twice from one copy in LDS, as 16-byte fragments for K S and
+// through the transpose load for K^T R: state tile t holds the channels
+// 32 (t/2) + 8 (row/4) + 4 (t%2) + row%4, so the eight channels of a lane's fragment are
+// consecutive, and the state's own registers are the operand of the next product.
+//
+// PRECISION.  The products with the state run on fp16 pieces: K and Q in one (bf16 inputs,
+// exact) or two (fp32), the state and what is added to it in two, 2^-22 each.  A row of K or
+// Q carries a power of two that brings its largest entry into [1/2, 1); a column of the state
+// is kept in registers multiplied by a power of two (up), which changes only when the column
+// leaves [2^-2, 2^13] or an added term 2^8: 32 terms below 2^8 then stay below the fp16
+// limit of 65504.  The 32 x 32 products run on three bf16 pieces (A R on two where o is bf16,
+// whose own rounding is 2^-8); the unit diagonal of the inverse is added in fp32.
+#include <type_traits>
+
+#include "gdr_launch.h"
+#include "gdr_mfma.h"
+
+namespace gdr {
+namespace {
+
+constexpr int C = 32;          // tokens of a chunk
+constexpr int COLS = 64;       // value columns of a workgroup
+constexpr int LDT = C + 8;     // pitch (bf16) of the 32 x 32 matrices: 16-byte reads without conflicts
+
+enum Mode { FWD, CKPT, BWD };
+
+struct ChainArgs {
+    const void *q, *k, *v;     // v: forward
+    const float *g, *beta, *first;  // first: state_in / d_state_out or nullptr
+    const float *d_o;          // backward
+    void *o;                   // forward
+    float *last;               // state_out / d_state_in
+    float *saved;              // ckpt / work
+    float *rows;               // resid / Y
+    const int *lengths;
+    float scale;
+    int B, T, Hk, H, V;
+};
+
+// fp16 and bf16 pieces of an input row.
+template <typename Tin> constexpr int input_pieces() { return std::is_same<Tin, float>::value ? 2 : 1; }
+template <typename Tin> constexpr int input_pieces_b() { return std::is_same<Tin, float>::value ? 3 : 1; }
+
+template <int K, int NP, int NA>
+struct Smem {
+    uint16_t k[2][NP][C][K + 16], q[2][NP][C][K + 16];
+    // inverse - I and A as [row][token slot] (backward: transposed); token t < 16 has slot
+    // 8 (t/4) + t%4, token 16 + t four more: a fragment's eight tokens are consecutive
+    uint16_t t[2][3][C][LDT], a[2][NA][C][LDT];
+    float x[2][C][36];         // x[j][i] = the triangular matrix at (i, j)
+    float p[2][C][34];         // P; column 32: gamma (33: not used)
+    float d[2][16][20];        // the inverse's diagonal blocks
+    float vec[4][4][C];        // gamma | beta P_C (backward: P_C) | beta | gamma beta
+    float con[4][3][C];        // vec 0, 1 (backward: 1, -3) with K's row factors; scale gamma with Q's
+    float kf[C], qf[C];        // row factors: K's (K wave), Q's (Q wave)
+};
+
+// Eight input elements of a row.
+template <typename Tin> struct Raw;
+template <> struct Raw<uint16_t> {
+    u32x4 x;
+    __device__ void load(const uint16_t *p) { x = *reinterpret_cast<const u32x4 *>(p); }
+    // the largest magnitude, as fp32 bits
+    __device__ uint32_t top() const
+    {
+        typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+        u16x2 m = __builtin_bit_cast(u16x2, x[0] & 0x7fff7fffu);
+#pragma unroll
+        for (int e = 1; e < 4; ++e)
+            m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, x[e] & 0x7fff7fffu));
+        return static_cast<uint32_t>(m[0] > m[1] ? m[0] : m[1]) << 16;
+    }
+    __device__ void planes(float f, float m1, s16x8 (&out)[1]) const
+    {
+        split8h<1>(f32x4{bf16_lo(x[0]) * f, bf16_hi(x[0]) * f, bf16_lo(x[1]) * f, bf16_hi(x[1]) * f},
+                   f32x4{bf16_lo(x[2]) * f, bf16_hi(x[2]) * f, bf16_lo(x[3]) * f, bf16_hi(x[3]) * f}, out, m1);
+    }
+    __device__ void bf16(s16x8 (&out)[1]) const { out[0] = __builtin_bit_cast(s16x8, x); }
+    __device__ void clear() { x = u32x4{0, 0, 0, 0}; }
+};
+template <> struct Raw<float> {
+    f32x4 x, y;
+    __device__ void load(const float *p)
+    {
+        x = *reinterpret_cast<const f32x4 *>(p);
+        y = *reinterpret_cast<const f32x4 *>(p + 4);
+    }
+    __device__ uint32_t top() const
+    {
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            m = max(m, max(__float_as_uint(x[e]) & 0x7fffffffu, __float_as_uint(y[e]) & 0x7fffffffu));
+        return m;
+    }
+    __device__ void planes(float f, float m1, s16x8 (&out)[2]) const { split8h<2>(x * f, y * f, out, m1); }
+    __device__ void bf16(s16x8 (&out)[3]) const { split8<3>(x, y, out); }
+    __device__ void clear() { x = y = f32x4{0.f, 0.f, 0.f, 0.f}; }
+};
+
+// The exponent e of a row or column whose largest magnitude has these fp32 bits: 2^-e brings
+// it into [1/2, 1).  0 for a largest of 0, infinity or NaN; kept to what 2^e and 2^-e hold.
+__device__ __forceinline__ int exponent(uint32_t bits)
+{
+    const int e = static_cast<int>(bits >> 23);
+    return bits == 0 || e == 255 ? 0 : min(max(e - 126, -120), 120);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// Two rows' elements of one column.
+__device__ __forceinline__ void put2(float *p, unsigned at, unsigned stride, float x, float y)
+{
+    p[at] = x;
+    (p + stride)[at] = y;
+}
+__device__ __forceinline__ void put2(uint16_t *p, unsigned at, unsigned stride, float x, float y)
+{
+    const uint32_t u = pk_bf16(x, y);
+    p[at] = static_cast<uint16_t>(u);
+    (p + stride)[at] = static_cast<uint16_t>(u >> 16);
+}
+
+// What every wave of a workgroup knows.
+struct Place {
+    int lane, row, quad;  // lane % 16, lane / 16
+    int b, h, kh;
+    int L, n;             // tokens and chunks of this row
+    size_t tok0;
+};
+
+// Decays of chunk s + 3: lane j < 32 walks down column j of P, lane 32 down gamma.
+template <bool BACK, typename SM>
+__device__ __forceinline__ void decay_wave(SM &sm, const ChainArgs &a, const Place &w)
+{
+    float g[2], be[2];
+    auto load = [&](int s, int at) {
+        const int c = BACK ? w.n - 1 - s : s, t = c * C + w.lane;
+        g[at] = be[at] = 0.f;  // behind the end: no decay, nothing written
+        if (s < w.n && w.lane < C && t < w.L) {
+            const size_t i = (w.tok0 + t) * a.H + w.h;
+            g[at] = a.g[i];
+            be[at] = a.beta[i];
+        }
+    };
+    const int col = min(w.lane, C + 1);
+    auto body = [&](int s, auto at) {
+        if (s < w.n) {
+            const float alpha = expf(g[at]), beta = be[at];
+            load(s + 2, at);
+            float p = w.lane == C ? 1.f : 0.f;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const float next = p * wkv7::lane_bcast(alpha, i);
+                p = i == w.lane ? 1.f : next;
+                sm.p[s & 1][i][col] = p;
+            }
+            wave_lds_fence();
+            if (w.lane < C) {
+                const float gamma = sm.p[s & 1][w.lane][C];
+                sm.vec[s & 3][0][w.lane] = gamma;
+                sm.vec[s & 3][1][w.lane] = BACK ? p : p * beta;
+                sm.vec[s & 3][2][w.lane] = beta;
+                sm.vec[s & 3][3][w.lane] = gamma * beta;
+            }
+        }
+        __syncthreads();
+    };
+    load(0, 0);
+    load(1, 1);
+    for (int s = 0;;) {
+        body(s, std::integral_constant<int, 0>{});
+        if (++s == w.n + 3)
+            break;
+        body(s, std::integral_constant<int, 1>{});
+        if (++s == w.n + 3)
+            break;
+    }
+}
+
+// x of lane `J` of this lane's row of 16.
+template <int J>
+__device__ __forceinline__ float row_lane(float x)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + J, 0xf, 0xf, true));
+}
+
+// One step of the substitution: c[i] -= M(i, J) c[J] for i > J, then the next.  Lane (column
+// of the inverse) r of a row of 16 holds M(i, r) in m[i].
+template <int J>
+__device__ __forceinline__ void eliminate(float (&c)[16], const float (&m)[16])
+{
+    if constexpr (J < 15) {
+        const float x = -c[J];
+#pragma unroll
+        for (int i = J + 1; i < 16; ++i)
+            c[i] = fmaf(row_lane<J>(m[i]), x, c[i]);
+        eliminate<J + 1>(c, m);
+    }
+}
+
+// The inverse of chunk s + 1, less the unit diagonal.
+template <bool BACK, typename SM>
+__device__ __forceinline__ void inverse_wave(SM &sm, const Place &w)
+{
+    const int row = w.row, quad = w.quad, blk = quad & 1;
+    for (int it = -3; it < w.n; ++it) {
+        const int s = it + 1;
+        if (s >= 0 && s < w.n) {
+            const float(*x)[36] = sm.x[s & 1];
+            // lanes 16 blk + r (and the upper 32 again): column r of diagonal block blk
+            float c[16], m[16];
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const f32x4 u = *reinterpret_cast<const f32x4 *>(&x[16 * blk + row][16 * blk + i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    m[i + e] = u[e];
+                    c[i + e] = i + e == row ? 1.f : 0.f;
+                }
+            }
+            // the block below, read ahead
+            float low[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                low[e] = BACK ? x[4 * e + quad][16 + row] : x[row][16 + 4 * e + quad];
+            eliminate<0>(c, m);
+            if (w.lane < 32)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    sm.d[blk][i][row] = c[i];
+            wave_lds_fence();
+            // the block below the diagonal, -D1 M D0 (backward: its rows; forward: transposed)
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f}, below = acc;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int u = 4 * e + quad;
+                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(low[e], BACK ? sm.d[0][u][row] : sm.d[1][row][u], acc, 0, 0, 0);
+            }
+            u32x2 out[3];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                f32x4 dd;
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    dd[f] = BACK ? sm.d[e][4 * quad + f][row] : sm.d[e][row][4 * quad + f];
+                    dd[f] = 4 * quad + f == row ? 0.f : dd[f];
+                }
+                split4<3>(dd, out);
+#pragma unroll
+                for (int p = 0; p < 3; ++p)
+                    *reinterpret_cast<u32x2 *>(&sm.t[s & 1][p][16 * e + row][8 * quad + 4 * e]) = out[p];
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int u = 4 * quad + e;
+                below = __builtin_amdgcn_mfma_f32_16x16x4f32(BACK ? sm.d[1][row][u] : sm.d[0][u][row], -acc[e], below, 0,
+                                                             0, 0);
+            }
+            split4<3>(below, out);
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+                *reinterpret_cast<u32x2 *>(&sm.t[s & 1][p][BACK ? row : 16 + row][8 * quad + (BACK ? 4 : 0)]) = out[p];
+        }
+        __syncthreads();
+    }
+}
+
+// The K wave (IS_Q false) and the Q wave: products of the rows of chunk s + 2; the rows
+// themselves go to LDS one chunk later.
+template <typename Tin, int K, int NA, bool BACK, bool IS_Q, typename SM>
+__device__ __forceinline__ void rows_wave(SM &sm, const ChainArgs &a, const Place &w)
+{
+    constexpr int NP = input_pieces<Tin>(), NB = input_pieces_b<Tin>(), NM = K / 32;
+    constexpr int DEPTH = std::is_same<Tin, float>::value ? 1 : 2;  // chunks of raw rows in flight
+    const int row = w.row, quad = w.quad;
+    const float m1 = minus_one();
+    const size_t stride = static_cast<size_t>(a.Hk) * K;
+    const Tin *kp = static_cast<const Tin *>(a.k) + (w.tok0 * a.Hk + w.kh) * K + 8 * quad;
+    const Tin *qp = static_cast<const Tin *>(a.q) + (w.tok0 * a.Hk + w.kh) * K + 8 * quad;
+    auto chunk = [&](int s) { return BACK ? w.n - 1 - s : s; };
+    Raw<Tin> kr[DEPTH][2][NM], qr[IS_Q ? DEPTH : 1][2][NM];
+    auto load = [&](int s, int at) {
+        if (s >= w.n)
+            return;
+#pragma unroll
+        for (int tau = 0; tau < 2; ++tau) {
+            const int t = min(chunk(s) * C + 16 * tau + row, w.L - 1);
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                kr[at][tau][m].load(kp + t * stride + 32 * m);
+                if constexpr (IS_Q)
+                    qr[at][tau][m].load(qp + t * stride + 32 * m);
+            }
+        }
+    };
+    s16x8 held[2][NM][NP];  // rows that go to LDS in the next iteration
+    u32x2 mat[3][NA];       // and tiles of A
+    // the rows of a tile: their power of two, fp16 fragments to `f`; returns what undoes the power
+    auto convert = [&](const Raw<Tin>(&r)[NM], s16x8(&f)[NM][NP]) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+            top = max(top, r[m].top());
+        const int e = exponent(quad_max(top));
+        const float down = pow2(-e);
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+            r[m].planes(down, m1, f[m]);
+        return pow2(e);
+    };
+    auto body = [&](int it, auto at) {
+        const int s = it + 2;
+        if (s >= 1 && s <= w.n) {
+            const int slot = (s - 1) & 1;
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau)
+#pragma unroll
+                for (int m = 0; m < NM; ++m)
+#pragma unroll
+                    for (int p = 0; p < NP; ++p)
+                        *reinterpret_cast<s16x8 *>(IS_Q ? &sm.q[slot][p][16 * tau + row][32 * m + 8 * quad]
+                                                        : &sm.k[slot][p][16 * tau + row][32 * m + 8 * quad]) =
+                            held[tau][m][p];
+            if constexpr (IS_Q)
+#pragma unroll
+                for (int e = 0; e < 3; ++e) {
+                    const int ti = e > 0, tj = e > 1;
+#pragma unroll
+                    for (int p = 0; p < NA; ++p)
+                        *reinterpret_cast<u32x2 *>(
+                            &sm.a[slot][p][16 * (BACK ? tj : ti) + row][8 * quad + 4 * (BACK ? ti : tj)]) = mat[e][p];
+                }
+        }
+        if (s >= 0 && s < w.n) {
+            const int t0 = chunk(s) * C + row;
+            f32x4 acc[3];
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (chunk(s) * C + C > w.L)
+#pragma unroll
+                for (int tau = 0; tau < 2; ++tau)
+                    if (t0 + 16 * tau >= w.L)
+#pragma unroll
+                        for (int m = 0; m < NM; ++m) {
+                            kr[at][tau][m].clear();
+                            if constexpr (IS_Q)
+                                qr[at][tau][m].clear();
+                        }
+            // lane: column of the tile; registers: rows 4 quad ..  The Q wave's forward tiles
+            // are transposed, as A's rows are stored.
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                s16x8 kb[2][NB], qb[2][NB];
+#pragma unroll
+                for (int tau = 0; tau < 2; ++tau) {
+                    kr[at][tau][m].bf16(kb[tau]);
+                    if constexpr (IS_Q)
+                        qr[at][tau][m].bf16(qb[tau]);
+                }
+#pragma unroll
+                for (int e = 0; e < 3; ++e) {
+                    const int ti = e > 0, tj = e > 1;
+                    if constexpr (!IS_Q)
+                        mma<NB, NB>(acc[e], kb[ti], kb[tj]);
+                    else if constexpr (BACK)
+                        mma<NB, NB>(acc[e], qb[ti], kb[tj]);
+                    else
+                        mma<NB, NB>(acc[e], kb[tj], qb[ti]);
+                }
+            }
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau) {
+                float f;
+                if constexpr (IS_Q)
+                    f = convert(qr[at][tau], held[tau]);
+                else
+                    f = convert(kr[at][tau], held[tau]);
+                if (quad == 0)
+                    (IS_Q ? sm.qf : sm.kf)[16 * tau + row] = f;
+            }
+            load(s + DEPTH, at);
+            wave_lds_fence();
+            const float(*P)[34] = sm.p[s & 1];
+            const float *beta = sm.vec[s & 3][2];
+            if (w.lane < C) {
+                const int l = w.lane;
+                if constexpr (IS_Q) {
+                    sm.con[s & 3][2][l] = a.scale * sm.vec[s & 3][0][l] * sm.qf[l];
+                } else {
+                    sm.con[s & 3][0][l] = (BACK ? sm.vec[s & 3][1][l] : sm.vec[s & 3][0][l]) * sm.kf[l];
+                    sm.con[s & 3][1][l] = (BACK ? -sm.vec[s & 3][3][l] : sm.vec[s & 3][1][l]) * sm.kf[l];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 3; ++e) {
+                const int ti = e > 0, tj = e > 1;
+                f32x4 v;
+                if constexpr (IS_Q && !BACK) {
+                    const int i = 16 * ti + row, j0 = 16 * tj + 4 * quad;
+                    const f32x4 be = *reinterpret_cast<const f32x4 *>(&beta[j0]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float y = P[i][j0 + r] * be[r] * (acc[e][r] * a.scale);
+                        v[r] = j0 + r <= i ? y : 0.f;
+                    }
+                } else {
+                    const int i0 = 16 * ti + 4 * quad, j = 16 * tj + row;
+                    const f32x4 be = *reinterpret_cast<const f32x4 *>(&beta[i0]);
+                    const float bj = beta[j];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float y = P[i0 + r][j] * (IS_Q ? a.scale : BACK ? be[r] : bj) * acc[e][r];
+                        v[r] = (IS_Q ? j <= i0 + r : j < i0 + r) ? y : 0.f;
+                    }
+                }
+                if constexpr (IS_Q)
+                    split4<NA>(v, mat[e]);
+                else
+                    *reinterpret_cast<f32x4 *>(&sm.x[s & 1][16 * tj + row][16 * ti + 4 * quad]) = v;
+            }
+        }
+        __syncthreads();
+    };
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i)
+        load(i, i);
+    // the buffer in use alternates from chunk 0, which iteration -2 takes
+    for (int it = -3;;) {
+        body(it, std::integral_constant<int, DEPTH - 1>{});
+        if (++it == w.n)
+            break;
+        body(it, std::integral_constant<int, 0>{});
+        if (++it == w.n)
+            break;
+    }
+}
+
+template <typename Tin, typename Tout, int K, int MODE>
+__global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
+{
+    constexpr bool BACK = MODE == BWD;
+    constexpr int NP = input_pieces<Tin>(), NM = K / 32, NT = K / 16;
+    constexpr int NA = !BACK && std::is_same<Tout, uint16_t>::value ? 2 : 3;  // bf16 pieces in A R
+    __shared__ Smem<K, NP, NA> sm;
+
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const unsigned item = xcd_item(blockIdx.x, gridDim.x), nblk = a.V / COLS;
+    const unsigned head = item / nblk;
+    Place w;
+    w.lane = threadIdx.x & 63;
+    w.row = w.lane & 15;
+    w.quad = w.lane >> 4;
+    w.b = head / a.H;
+    w.h = head % a.H;
+    w.kh = w.h / (a.H / a.Hk);
+    w.L = a.lengths ? min(max(a.lengths[w.b], 0), a.T) : a.T;
+    w.n = (w.L + C - 1) / C;
+    w.tok0 = static_cast<size_t>(w.b) * a.T;
+
+    for (unsigned i = threadIdx.x; i < sizeof(sm.t) / 4; i += 512)
+        reinterpret_cast<uint32_t *>(sm.t)[i] = 0;  // the blocks above the diagonal stay 0
+    for (unsigned i = threadIdx.x; i < sizeof(sm.a) / 4; i += 512)
+        reinterpret_cast<uint32_t *>(sm.a)[i] = 0;
+    __syncthreads();
+
+    if (wave == 7) {
+        decay_wave<BACK>(sm, a, w);
+        return;
+    }
+    if (wave == 6) {
+        inverse_wave<BACK>(sm, w);
+        return;
+    }
+    if (wave == 5) {
+        rows_wave<Tin, K, NA, BACK, true>(sm, a, w);
+        return;
+    }
+    if (wave == 4) {
+        rows_wave<Tin, K, NA, BACK, false>(sm, a, w);
+        return;
+    }
+
+    // -------------------------------------------------------------------- consumers
+    const int lane = w.lane, row = w.row, quad = w.quad, n = w.n, L = w.L;
+    const float m1 = minus_one();
+    const int col = (item % nblk) * COLS + 16 * wave + row;
+    const size_t vs = static_cast<size_t>(a.H) * a.V;
+    // [b, 0, h, 0] of v, o, resid, d_o, and this lane's place in the rows of a chunk
+    const size_t row0 = (w.tok0 * a.H + w.h) * a.V;
+    const unsigned at0 = static_cast<unsigned>(4 * quad * vs + col), vs4 = static_cast<unsigned>(vs);
+    const size_t st0 = static_cast<size_t>(head) * K * a.V + col;  // [b, h, 0, col] of a state
+    auto channel = [&](int t, int r) { return 32 * (t >> 1) + 8 * quad + 4 * (t & 1) + r; };
+    using Trow = typename std::conditional<BACK, float, Tin>::type;
+    const Trow *in = static_cast<const Trow *>(BACK ? static_cast<const void *>(a.d_o) : a.v) + row0;  // + at0: this lane's rows
+
+    f32x4 S[NT];  // the state (backward: its gradient) times up
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            S[t][r] = a.first ? a.first[st0 + static_cast<size_t>(channel(t, r)) * a.V] : 0.f;
+    float up = 1.f, down = 1.f;  // 2^e and 2^-e, one e for each column
+    int scale_e = 0;
+    // Bring the column's scale back if an entry of S or an added term (at most `term`) asks for
+    // it.  A column's entries and terms sit in four lanes: too large in one of them, or too
+    // small in all four, is seen in the lanes' votes; maxima are formed only then.
+    auto rescale = [&](float term) -> float {
+        float top = 0.f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; r += 2)
+                top = fmaxf(fmaxf(fabsf(S[t][r]), fabsf(S[t][r + 1])), top);
+        unsigned long long big = __ballot(top >= 0x1p-2f);
+        big |= big >> 32;
+        big |= big >> 16;
+        if ((big & 0xffffu) == 0xffffu && !__any(!(top <= 0x1p13f) || !(term <= 0x1p8f)))
+            return 1.f;
+        top = __uint_as_float(quad_max(__float_as_uint(top)));
+        term = __uint_as_float(quad_max(__float_as_uint(term)));
+        const float all = fmaxf(top, 0.125f * term);
+        const bool off = (top < 0x1p-2f && all > 0.f) || !(top <= 0x1p13f) || !(term <= 0x1p8f);
+        // to [4, 8); up stays within what its reciprocal holds
+        int e = off && all < __builtin_huge_valf() ? 3 - exponent(__float_as_uint(all)) : 0;
+        e = min(max(scale_e + e, -120), 120) - scale_e;
+        scale_e += e;
+        up = pow2(scale_e);
+        down = pow2(-scale_e);
+        const float f = ldexpf(1.f, e);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            S[t] *= f;
+        return f;
+    };
+    rescale(0.f);
+
+    Trow next[2][4];
+    auto load = [&](int s) {
+        const int first = (BACK ? n - 1 - s : s) * C;
+        const Trow *p = in + first * vs;
+        if (first + C <= L) {
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    next[tau][r] = (p + (16 * tau + r) * vs)[at0];
+        } else {
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    next[tau][r] = first + 16 * tau + 4 * quad + r < L ? (p + (16 * tau + r) * vs)[at0] : Trow{0};
+        }
+    };
+    // rows of a chunk, to out[t][col]
+    auto store = [&](auto *out, int first, const f32x4(&x)[2]) {
+        auto *p = out + row0 + first * vs;
+        if (first + C <= L) {
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau)
+#pragma unroll
+                for (int r = 0; r < 4; r += 2)
+                    put2(p + (16 * tau + r) * vs, at0, vs4, x[tau][r], x[tau][r + 1]);
+        } else {
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (first + 16 * tau + 4 * quad + r < L)
+                        store_elem(p + (16 * tau + r) * vs, at0, x[tau][r]);
+        }
+    };
+    if (n > 0)
+        load(0);
+    __syncthreads();
+    __syncthreads();
+    __syncthreads();
+    for (int s = 0; s < n; ++s) {
+        const int slot = s & 1, c = BACK ? n - 1 - s : s;
+        f32x4 v[2];
+#pragma unroll
+        for (int tau = 0; tau < 2; ++tau)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                v[tau][r] = load_elem(&next[tau][r], 0);
+        if (s + 1 < n)
+            load(s + 1);
+        // the state on entering a block of 64 tokens (backward: the gradient behind it), in tile order
+        if (MODE == CKPT ? (c & 1) == 0 : MODE == BWD && ((c & 1) == 1 || c == n - 1)) {
+            const int nsaved = (a.T + kBlock - 1) / kBlock;
+            float *to = a.saved + ((static_cast<size_t>(w.b) * nsaved + c / 2) * a.H + w.h) * K * a.V +
+                        static_cast<size_t>(col / 16) * (16 * K) + 4 * lane;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                *reinterpret_cast<f32x4 *>(to + 256 * t) = S[t] * down;
+        }
+        f32x4 con[3][2];
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau)
+                con[x][tau] = *reinterpret_cast<const f32x4 *>(&sm.con[s & 3][x][16 * tau + 4 * quad]);
+        const float gC = sm.vec[s & 3][0][C - 1];
+
+        // products with the state
+        f32x4 ks[2], qs[2];
+#pragma unroll
+        for (int tau = 0; tau < 2; ++tau)
+            ks[tau] = qs[tau] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            s16x8 Sp[2];
+            split8h<2>(S[2 * m], S[2 * m + 1], Sp, m1);
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau) {
+                s16x8 f[NP];
+#pragma unroll
+                for (int p = 0; p < NP; ++p)
+                    f[p] = lds8(&sm.k[slot][p][16 * tau + row][32 * m + 8 * quad]);
+                mmah<NP, 2>(ks[tau], f, Sp);
+                if constexpr (!BACK) {
+#pragma unroll
+                    for (int p = 0; p < NP; ++p)
+                        f[p] = lds8(&sm.q[slot][p][16 * tau + row][32 * m + 8 * quad]);
+                    mmah<NP, 2>(qs[tau], f, Sp);
+                }
+            }
+        }
+#pragma unroll
+        for (int tau = 0; tau < 2; ++tau) {
+            ks[tau] *= down;
+            qs[tau] *= down;
+        }
+        // the 32 x 32 matrix x times the rows in zp, on top of out
+        auto apply = [&](const auto &x, const auto &zp, f32x4(&out)[2]) {
+            constexpr int NZ = std::extent<std::remove_reference_t<decltype(zp)>>::value;
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau) {
+                s16x8 f[NZ];
+#pragma unroll
+                for (int p = 0; p < NZ; ++p)
+                    f[p] = lds8(&x[p][16 * tau + row][8 * quad]);
+                mma<NZ, NZ>(out[tau], f, zp);
+            }
+        };
+        // K^T or Q^T of state tile t
+        auto transposed = [&](const uint16_t(&x)[NP][C][K + 16], int t, s16x8(&f)[NP]) {
+            const int at = 32 * (t >> 1) + 8 * (lane & 3) + 4 * (t & 1), r = 4 * quad + (row >> 2);
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+                f[p] = cat(tr4(&x[p][r][at]), tr4(&x[p][16 + r][at]));
+        };
+        auto largest = [&](const f32x4(&x)[2], float top) {
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau)
+#pragma unroll
+                for (int r = 0; r < 4; r += 2)
+                    top = fmaxf(fmaxf(fabsf(x[tau][r]), fabsf(x[tau][r + 1])), top);
+            return top;
+        };
+
+        f32x4 R[2], u[2];
+        s16x8 zp[3], up2[2];
+        if constexpr (!BACK) {
+            f32x4 O[2];
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    R[tau][r] = fmaf(-con[0][tau][r], ks[tau][r], v[tau][r]);
+            split8<3>(R[0], R[1], zp);
+            apply(sm.t[slot], zp, R);
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau)
+                u[tau] = con[1][tau] * (R[tau] * up);
+            const float f = rescale(largest(u, 0.f));
+            u[0] *= f;
+            u[1] *= f;
+            split8h<2>(u[0], u[1], up2, m1);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                s16x8 kt[NP];
+                transposed(sm.k[slot], t, kt);
+                S[t] *= gC;
+                mmah<NP, 2>(S[t], kt, up2);
+            }
+            s16x8 rp[NA];
+            split8<NA>(R[0], R[1], rp);
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau)
+                O[tau] = con[2][tau] * qs[tau];
+            apply(sm.a[slot], rp, O);
+            store(static_cast<Tout *>(a.o), c * C, O);
+            if (MODE == CKPT)
+                store(a.rows, c * C, R);
+        } else {
+            f32x4 y[2];
+            s16x8 yp[2];
+            split8<3>(v[0], v[1], zp);
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau)
+                R[tau] = con[0][tau] * ks[tau];
+            apply(sm.a[slot], zp, R);
+            split8<3>(R[0], R[1], zp);
+            apply(sm.t[slot], zp, R);
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau) {
+                u[tau] = con[1][tau] * (R[tau] * up);
+                y[tau] = con[2][tau] * (v[tau] * up);
+            }
+            store(a.rows, c * C, R);
+            const float f = rescale(largest(u, largest(y, 0.f)));
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau) {
+                u[tau] *= f;
+                y[tau] *= f;
+            }
+            split8h<2>(u[0], u[1], up2, m1);
+            split8h<2>(y[0], y[1], yp, m1);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                s16x8 x[NP];
+                S[t] *= gC;
+                transposed(sm.q[slot], t, x);
+                mmah<NP, 2>(S[t], x, yp);
+                transposed(sm.k[slot], t, x);
+                mmah<NP, 2>(S[t], x, up2);
+            }
+        }
+        __syncthreads();
+    }
+    if (n > 0 || a.first != a.last)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                a.last[st0 + static_cast<size_t>(channel(t, r)) * a.V] = S[t][r] * down;
+}
+
+template <typename Tin, typename Tout, int MODE>
+hipError_t launch_k(const ChainArgs &a, int K, hipStream_t stream)
+{
+    const dim3 grid(static_cast<unsigned>(static_cast<long long>(a.B) * a.H * (a.V / COLS))), block(512);
+    if (K == 64)
+        hipLaunchKernelGGL((gdr_chain_kernel<Tin, Tout, 64, MODE>), grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((gdr_chain_kernel<Tin, Tout, 128, MODE>), grid, block, 0, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_chain(const SeqArgs &p, hipStream_t stream)
+{
+    ChainArgs a = {};
+    a.q = p.q; a.k = p.k; a.v = p.v; a.g = p.g; a.beta = p.beta; a.first = p.state_in;
+    a.o = p.o; a.last = p.state_out; a.saved = p.ckpt; a.rows = p.resid; a.lengths = p.lengths;
+    a.scale = p.scale;
+    a.B = p.B; a.T = p.T; a.Hk = p.Hk; a.H = p.H; a.V = p.V;
+    if (p.ckpt)
+        return p.in_bf16 ? launch_k<uint16_t, float, CKPT>(a, p.K, stream) : launch_k<float, float, CKPT>(a, p.K, stream);
+    if (p.in_bf16)
+        return p.o_bf16 ? launch_k<uint16_t, uint16_t, FWD>(a, p.K, stream) : launch_k<uint16_t, float, FWD>(a, p.K, stream);
+    return p.o_bf16 ? launch_k<float, uint16_t, FWD>(a, p.K, stream) : launch_k<float, float, FWD>(a, p.K, stream);
+}
+
+hipError_t launch_backward_chain(const BwdArgs &p, hipStream_t stream)
+{
+    ChainArgs a = {};
+    a.q = p.q; a.k = p.k; a.g = p.g; a.beta = p.beta; a.first = p.d_state_out; a.d_o = p.d_o;
+    a.last = p.d_state_in; a.saved = p.work; a.rows = p.dv;
+    a.scale = p.scale;
+    a.B = p.B; a.T = p.T; a.Hk = p.Hk; a.H = p.H; a.V = p.V;
+    return p.in_bf16 ? launch_k<uint16_t, float, BWD>(a, p.K, stream) : launch_k<float, float, BWD>(a, p.K, stream);
+}
+
+}  // namespace gdr

@@ -2,11 +2,12 @@
 
 Tolerances (relative L2; see parity.py for the per-head and per-element bounds).  An fp32
 result is a sum of products in fp32 (2^-24 each way) in which some operands were split into
-two bf16 pieces: a piece rounds to half a step (2^-9 relative), two leave at most 2^-18 =
-3.8e-6 and 7e-7 in the root mean square.  At most three such operands stand between an
-input and an output (the state, the residual and the triangular inverse), 3 x 7e-7 = 2.1e-6,
-and the rule does not amplify an error (unit keys, beta <= 1, decay <= 1).  4e-6 leaves the
-accumulation of the sums as much again.  A bf16 output adds half a step, 2^-8 relative.
+pieces that keep them to 2^-22 (two fp16 pieces, 2^-11 each) or 2^-24 (three bf16 pieces).  At
+most four such operands stand between an input and an output (the state, the triangular inverse,
+the residual and what it adds to the state), 4 x 2^-22 = 1e-6, and the rule does not amplify an
+error (unit keys, beta <= 1, decay <= 1).  4e-6 leaves the accumulation of the sums (up to 128
+products and 32 tokens, each rounded) three times as much again.  A bf16 output adds half a
+step, 2^-8 relative.
 """
 import numpy as np
 import pytest
