@@ -59,7 +59,7 @@ extern "C" {
 #define GDR_MAX_V 512
 #define GDR_MAX_ROW 16777216
 #define GDR_MAX_T 1073741824
-#define GDR_MAX_BLOCKS 8388608
+#define GDR_MAX_BLOCKS 8000000
 #define GDR_MAX_COLUMNS 268435456
 
 /*

@@ -17,7 +17,7 @@ namespace {
 constexpr int kChainMinT = 9;
 
 static_assert(GDR_MAX_COLUMNS / 64 * 512ll < (1ll << 32) && GDR_MAX_COLUMNS / 32 * 64ll < (1ll << 32) &&
-                  GDR_MAX_BLOCKS * 256ll < (1ll << 32) &&
+                  GDR_MAX_BLOCKS * 512ll < (1ll << 32) &&
                   DRAFT_MAX_ROWS * 1024ll < (1ll << 32),
               "a launch must hold fewer than 2^32 threads");
 

@@ -90,8 +90,11 @@ __device__ __forceinline__ void fragment(const float *p, s16x8 (&f)[3])
     split8<3>(*reinterpret_cast<const f32x4 *>(p), *reinterpret_cast<const f32x4 *>(p + 4), f);
 }
 
+// Waves per SIMD: two workgroups share a compute unit with bf16 inputs (80 KB of LDS each).
+template <typename Tin> constexpr int grad_waves() { return std::is_same<Tin, float>::value ? 1 : 2; }
+
 template <typename Tin, int K>
-__global__ __launch_bounds__(256) void gdr_grad_kernel(BwdArgs p, int nblk)
+__global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArgs p, int nblk)
 {
     constexpr int NB = row_pieces<Tin>(), NT = K / 16;
     constexpr int UNITS = VB * K / 4 / 256;  // 16-byte units of a staged state, per thread
@@ -110,31 +113,31 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(BwdArgs p, int nblk)
     // The rows of K or Q to LDS, in bf16 pieces; rows behind the end are 0.
     auto stage_rows = [&](const void *src) {
         const Tin *x = static_cast<const Tin *>(src) + qk0;
-        for (int u = tid; u < TB * (K / 8); u += 256) {
-            const int t = u / (K / 8), c = 8 * (u % (K / 8));
-            s16x8 f[NB];
+        constexpr int N = TB * (K / 8) / 256, STEP = N < 4 ? N : 4;
 #pragma unroll
-            for (int i = 0; i < NB; ++i)
-                f[i] = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
-            if (t < live)
-                fragment(x + t * qs + c, f);
+        for (int i0 = 0; i0 < N; i0 += STEP) {
+            s16x8 f[STEP][NB];
 #pragma unroll
-            for (int i = 0; i < NB; ++i)
-                *reinterpret_cast<s16x8 *>(&sm.rows[i][t][c]) = f[i];
+            for (int i = 0; i < STEP; ++i) {
+                const int u = tid + 256 * (i0 + i), t = u / (K / 8), c = 8 * (u % (K / 8));
+                fragment(x + min(t, live - 1) * qs + c, f[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < STEP; ++i) {
+                const int u = tid + 256 * (i0 + i), t = u / (K / 8), c = 8 * (u % (K / 8));
+#pragma unroll
+                for (int y = 0; y < NB; ++y)
+                    *reinterpret_cast<s16x8 *>(&sm.rows[y][t][c]) = t < live ? f[i][y] : s16x8{0, 0, 0, 0, 0, 0, 0, 0};
+            }
         }
     };
-    // out[r] += this lane's channels of staged row 16 w + 4 quad + r times x
-    auto dot_rows = [&](const f32x4(&x)[NT], f32x4 &out) {
+    // element 16 t + row of staged row 16 w + 4 quad + r
+    auto element = [&](int t, int r) {
+        float y = 0.f;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float y = 0.f;
-#pragma unroll
-                for (int i = NB - 1; i >= 0; --i)
-                    y += load_elem(&sm.rows[i][16 * w + 4 * quad + r][16 * t + row], 0);
-                out[r] = fmaf(y, x[t][r], out[r]);
-            }
+        for (int i = NB - 1; i >= 0; --i)
+            y += load_elem(&sm.rows[i][16 * w + 4 * quad + r][16 * t + row], 0);
+        return y;
     };
 
     for (int hh = 0; hh < group; ++hh) {
@@ -167,23 +170,6 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(BwdArgs p, int nblk)
         const float *sp = p.ckpt + ((static_cast<size_t>(b) * nblk + blk) * p.H + h) * K * p.V + 4 * tid;
         const float *gp = p.work + ((static_cast<size_t>(b) * nblk + blk) * p.H + h) * K * p.V + 4 * tid;
 
-        f32x4 s4[UNITS], g4[UNITS], x4[3][2];  // dO, Y, R at columns 4 quad and 16 + 4 quad
-        auto load = [&](int v) {
-#pragma unroll
-            for (int i = 0; i < UNITS; ++i) {
-                s4[i] = *reinterpret_cast<const f32x4 *>(sp + static_cast<size_t>(v) * K + 1024 * i);
-                g4[i] = *reinterpret_cast<const f32x4 *>(gp + static_cast<size_t>(v) * K + 1024 * i);
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const size_t at = mrow + v + 16 * e;
-                const f32x4 z = {0.f, 0.f, 0.f, 0.f};
-                x4[0][e] = on ? *reinterpret_cast<const f32x4 *>(p.d_o + at) : z;
-                x4[1][e] = on ? *reinterpret_cast<const f32x4 *>(p.dv + at) : z;
-                x4[2][e] = on ? *reinterpret_cast<const f32x4 *>(p.resid + at) : z;
-            }
-        };
-        load(0);
         f32x4 dq[NT], dr[NT], dc[NT], e1[4], e2[4];  // dr, dc: the two parts of dk; e1, e2 transposed
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -196,6 +182,44 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(BwdArgs p, int nblk)
         const float beta = sm.beta[mine];
 
         for (int v = 0; v < p.V; v += VB) {
+            // (two workgroups share a compute unit: one multiplies while the other loads)
+            f32x4 s4[UNITS], g4[UNITS], x4[3][2];  // units of S and G; dO, Y, R at columns 4 quad and 16 + 4 quad
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const size_t at = mrow + v + 16 * e;
+                x4[0][e] = *reinterpret_cast<const f32x4 *>(p.d_o + at);
+                x4[1][e] = *reinterpret_cast<const f32x4 *>(p.dv + at);
+                x4[2][e] = *reinterpret_cast<const f32x4 *>(p.resid + at);
+            }
+#pragma unroll
+            for (int i = 0; i < UNITS; ++i) {
+                s4[i] = *reinterpret_cast<const f32x4 *>(sp + static_cast<size_t>(v) * K + 1024 * i);
+                g4[i] = *reinterpret_cast<const f32x4 *>(gp + static_cast<size_t>(v) * K + 1024 * i);
+            }
+            s16x8 fo[3], fv[3], fu[3];
+#pragma unroll
+            for (int x = 0; x < 3; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        x4[x][e][r] = on ? x4[x][e][r] : 0.f;
+            split8<3>(x4[0][0], x4[0][1], fo);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    db = fmaf(x4[1][e][r], x4[2][e][r], db);
+                x4[1][e] *= beta;
+                x4[2][e] *= beta;
+                if (on)
+                    *reinterpret_cast<f32x4 *>(p.dv + mrow + v + 16 * e) = x4[1][e];
+            }
+            split8<3>(x4[1][0], x4[1][1], fv);
+            split8<3>(x4[2][0], x4[2][1], fu);
+#pragma unroll
+            for (int x = 0; x < 3; ++x)
+                *reinterpret_cast<s16x8 *>(&sm.u[w][x][lane][0]) = fu[x];
 #pragma unroll
             for (int i = 0; i < UNITS; ++i) {
                 const int u = tid + 256 * i, jt = u / (4 * K), t = (u >> 6) % NT;
@@ -213,25 +237,6 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(BwdArgs p, int nblk)
                 for (int r = 0; r < 4; ++r)
                     gs = fmaf(s4[i][r], g4[i][r], gs);
             }
-            s16x8 fo[3], fv[3], fu[3];
-            split8<3>(x4[0][0], x4[0][1], fo);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    db = fmaf(x4[1][e][r], x4[2][e][r], db);
-                x4[1][e] *= beta;
-                x4[2][e] *= beta;
-                if (on)
-                    *reinterpret_cast<f32x4 *>(p.dv + mrow + v + 16 * e) = x4[1][e];
-            }
-            split8<3>(x4[1][0], x4[1][1], fv);
-            split8<3>(x4[2][0], x4[2][1], fu);
-#pragma unroll
-            for (int x = 0; x < 3; ++x)
-                *reinterpret_cast<s16x8 *>(&sm.u[w][x][lane][0]) = fu[x];
-            if (v + VB < p.V)
-                load(v + VB);
             __syncthreads();
             const int r0 = 4 * quad + (row >> 2);
 #pragma unroll
@@ -270,16 +275,23 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(BwdArgs p, int nblk)
             if (t > (w | 1))
                 continue;  // never read
             if (t <= w) {
-                float mid = sm.a[mine];
-                for (int i = t + 1; i < w; ++i)
-                    mid *= sm.bp[i];
+                f32x4 P;
+                if (t == w) {
+                    P = f32x4{sm.diag[w][row][4 * quad], sm.diag[w][row][4 * quad + 1], sm.diag[w][row][4 * quad + 2],
+                              sm.diag[w][row][4 * quad + 3]};
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int j = 4 * quad + r;
-                    const float P = t == w ? sm.diag[w][row][j] : mid * sm.b[16 * t + j];
-                    const float x1 = P * (p.scale * e1[t][r]), x2 = -P * e2[t][r];
-                    e1[t][r] = t < w || j <= row ? x1 : 0.f;
-                    e2[t][r] = t < w || j < row ? x2 : 0.f;
+                    for (int r = 0; r < 4; ++r) {
+                        e1[t][r] = 4 * quad + r <= row ? P[r] * (p.scale * e1[t][r]) : 0.f;
+                        e2[t][r] = 4 * quad + r < row ? -P[r] * e2[t][r] : 0.f;
+                    }
+                } else {
+                    float mid = sm.a[mine];
+#pragma unroll
+                    for (int i = 1; i < 3; ++i)
+                        mid *= i > t && i < w ? sm.bp[i] : 1.f;
+                    P = mid * *reinterpret_cast<const f32x4 *>(&sm.b[16 * t + 4 * quad]);
+                    e1[t] *= p.scale * P;
+                    e2[t] *= -P;
                 }
             }
             const int slot = 32 * (t >> 1) + 8 * quad + 4 * (t & 1);
@@ -329,27 +341,21 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(BwdArgs p, int nblk)
                 }
             }
         };
-        // q_i . dq_i while dq holds the states' part only
+        // e and f, while dq, dr and dc hold the states' parts only
         f32x4 ei, fj;
-        {
-            const Tin *q = static_cast<const Tin *>(p.q) + qk0 + row;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const Tin *qr = q + static_cast<size_t>(min(16 * w + 4 * quad + r, live - 1)) * qs;
-                float s = 0.f;
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    s = fmaf(load_elem(qr, 16 * t), dq[t][r], s);
-                ei[r] = s;
-            }
-        }
-        dot_rows(dr, ei);
-        fj = f32x4{0.f, 0.f, 0.f, 0.f};
-        dot_rows(dc, fj);
+        const Tin *q = static_cast<const Tin *>(p.q) + qk0 + row;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            ei[r] = wkv7::group16_sum(ei[r]);
-            fj[r] = wkv7::group16_sum(fj[r]);
+            const Tin *qr = q + static_cast<size_t>(min(16 * w + 4 * quad + r, live - 1)) * qs;
+            float s = 0.f, u = 0.f;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const float k = element(t, r);
+                s = fmaf(load_elem(qr, 16 * t), dq[t][r], fmaf(k, dr[t][r], s));
+                u = fmaf(k, dc[t][r], u);
+            }
+            ei[r] = wkv7::group16_sum(s);
+            fj[r] = wkv7::group16_sum(u);
         }
         if (row == 0) {
             *reinterpret_cast<f32x4 *>(&sm.e[16 * w + 4 * quad]) = ei;
@@ -440,15 +446,32 @@ __global__ __launch_bounds__(256) void gdr_grad_kernel(BwdArgs p, int nblk)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int t = 16 * w + 4 * quad + r;
-            if (t < live) {
-                float *q = p.dq + qk0 + t * qs + row, *k = p.dk + qk0 + t * qs + row;
+            float *dqr = p.dq + qk0 + min(t, live - 1) * qs + row, *dkr = p.dk + qk0 + min(t, live - 1) * qs + row;
+            float x[NT], y[NT];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                x[i] = dq[i][r];
+                y[i] = dr[i][r];
+            }
+            if (hh) {
+                float x0[NT], y0[NT];
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
-                    const float x = dq[i][r], y = dr[i][r];
-                    q[16 * i] = hh ? q[16 * i] + x : x;
-                    k[16 * i] = hh ? k[16 * i] + y : y;
+                    x0[i] = dqr[16 * i];
+                    y0[i] = dkr[16 * i];
+                }
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    x[i] += x0[i];
+                    y[i] += y0[i];
                 }
             }
+            if (t < live)
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    dqr[16 * i] = x[i];
+                    dkr[16 * i] = y[i];
+                }
         }
         __syncthreads();
     }
