@@ -191,7 +191,8 @@ def _out_arg(x, shape, device, name, dtypes=(torch.float32, torch.bfloat16)):
 
 def _int_rows(x, B, device, name):
     """A [B] int32 device tensor (converted from any integer tensor or sequence)."""
-    x = torch.as_tensor(x, device=device).to(torch.int32).contiguous()
+    if not (torch.is_tensor(x) and x.dtype is torch.int32 and x.device == device and x.is_contiguous()):
+        x = torch.as_tensor(x, device=device).to(torch.int32).contiguous()
     if x.shape != (B,):
         raise ValueError(f"{name} must have shape [{B}]")
     return x

@@ -3,8 +3,8 @@ from __future__ import annotations
 
 import torch
 
-from . import _check, _dt, _int_rows, _out_arg, _ptr, _stream, lib
-from .gdr import _on
+from . import _check, _dt, _int_rows, _out_arg, lib
+from .gdr import _good, _on, _output, _p, _stream
 
 I32, F32 = (torch.int32,), (torch.float32,)
 
@@ -25,20 +25,20 @@ def draft_verify(target, tokens, u, u_draw, *, draft=None, n_draft=None, out=Non
     if target.dim() != 3 or not target.is_cuda or not target.is_contiguous():
         raise ValueError("target must be a contiguous [B, N+1, vocab] GPU tensor")
     _dt(target)
-    B, N, vocab = target.shape[0], target.shape[1] - 1, target.shape[2]
-    dev = target.device
-    _out_arg(tokens, (B, N), dev, "tokens", I32)
-    _out_arg(u, (B, N), dev, "u", F32)
-    _out_arg(u_draw, (B,), dev, "u_draw", F32)
-    if draft is not None:
+    B, places, vocab = target.shape
+    N, dev = places - 1, target.device
+    if not (_good(tokens, (B, N), torch.int32, dev) and _good(u, (B, N), torch.float32, dev)
+            and _good(u_draw, (B,), torch.float32, dev)):
+        _out_arg(tokens, (B, N), dev, "tokens", I32)
+        _out_arg(u, (B, N), dev, "u", F32)
+        _out_arg(u_draw, (B,), dev, "u_draw", F32)
+    if draft is not None and not _good(draft, (B, N, vocab), target.dtype, dev):
         _out_arg(draft, (B, N, vocab), dev, "draft", (target.dtype,))
-    out = torch.empty((B, N + 1), dtype=torch.int32, device=dev) if out is None else out
-    _out_arg(out, (B, N + 1), dev, "out", I32)
-    kept = torch.empty((B,), dtype=torch.int32, device=dev) if kept is None else kept
-    _out_arg(kept, (B,), dev, "kept", I32)
+    out = _output(out, (B, places), dev, "out", torch.int32, I32)
+    kept = _output(kept, (B,), dev, "kept", torch.int32, I32)
     with _on(dev):
         n_draft = None if n_draft is None else _int_rows(n_draft, B, dev, "n_draft")
-        _check(lib().draft_verify(_ptr(target), _ptr(draft) if N else None, _dt(target), _ptr(tokens) if N else None,
-                                  _ptr(n_draft), _ptr(u) if N else None, _ptr(u_draw), _ptr(out), _ptr(kept),
-                                  B, N, vocab, _stream(dev)))
+        _check(lib().draft_verify(target.data_ptr(), _p(draft), _dt(target), tokens.data_ptr(), _p(n_draft),
+                                  u.data_ptr(), u_draw.data_ptr(), out.data_ptr(), kept.data_ptr(), B, N, vocab,
+                                  _stream(dev)))
     return out, kept

@@ -13,19 +13,18 @@ code pairs gdr_forward_ckpt with gdr_backward_ckpt.
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
-from . import _check, _dt, _int_rows, _out_arg, _ptr, _state_arg, _stream, lib
+from . import _check, _dt, _int_rows, _out_arg, _state_arg, lib
 
 F32 = (torch.float32,)
 BLOCK = 64  # tokens between two checkpoints
+_f32 = torch.float32
 
 
 def _on(device):
     """The device's own context, where another device is current."""
-    if device.index is None or device.index == torch.cuda.current_device():
+    if device.index == torch.cuda.current_device():
         return _SAME
     return torch.cuda.device(device)
 
@@ -41,43 +40,70 @@ class _Same:
 _SAME = _Same()
 
 
+def _stream(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _p(x):
+    return None if x is None else x.data_ptr()
+
+
+# A serving step is a few microseconds of kernel: each tensor is checked in one expression, and
+# only one that fails is looked at again to say why.
+def _good(x, shape, dtype, device):
+    return x.shape == shape and x.dtype is dtype and x.device == device and x.is_contiguous()
+
+
 def _check_qk(q, k, g, beta, H):
     if q.dim() != 4:
         raise ValueError(f"q must be [B, T, Hk, K], got {tuple(q.shape)}")
-    B, T, Hk, K = q.shape
-    dev = q.device
+    shape, dev = q.shape, q.device
+    B, T, Hk, K = shape
     if not q.is_cuda:
         raise ValueError("inputs must be on the GPU")
-    _dt(q)
-    if k.shape != q.shape or k.dtype != q.dtype or k.device != dev:
-        raise ValueError("q and k must share shape, dtype and device")
-    if not (q.is_contiguous() and k.is_contiguous()):
+    if not (_good(k, shape, q.dtype, dev) and q.is_contiguous()):
+        if k.shape != shape or k.dtype != q.dtype or k.device != dev:
+            raise ValueError("q and k must share shape, dtype and device")
         raise ValueError("inputs must be contiguous")
     if Hk < 1 or H % Hk:
         raise ValueError(f"the {Hk} query / key heads must divide the {H} value heads")
-    for name, x in (("g", g), ("beta", beta)):
-        _out_arg(x, (B, T, H), dev, name, F32)
+    gates = (B, T, H)
+    if not (_good(g, gates, _f32, dev) and _good(beta, gates, _f32, dev)):
+        _out_arg(g, gates, dev, "g", F32)
+        _out_arg(beta, gates, dev, "beta", F32)
     return B, T, Hk, K, dev
 
 
 def _check_inputs(q, k, v, g, beta):
     if v.dim() != 4:
         raise ValueError(f"v must be [B, T, H, V], got {tuple(v.shape)}")
-    H, V = v.shape[2:]
+    _, _, H, V = v.shape
     B, T, Hk, K, dev = _check_qk(q, k, g, beta, H)
-    if tuple(v.shape[:2]) != (B, T) or v.dtype != q.dtype or v.device != dev:
-        raise ValueError("v must match q in batch, tokens, dtype and device")
-    if not v.is_contiguous():
+    if not _good(v, (B, T, H, V), q.dtype, dev):
+        if v.shape[0] != B or v.shape[1] != T or v.dtype != q.dtype or v.device != dev:
+            raise ValueError("v must match q in batch, tokens, dtype and device")
         raise ValueError("inputs must be contiguous")
     return B, T, Hk, H, K, V, dev
 
 
-def _new(shape, device, dtype=torch.float32):
-    return torch.empty(shape, dtype=dtype, device=device)
+def _state(x, shape, device, name, new=False):
+    """A state argument, or (new) a fresh state in the place of None."""
+    if x is None:
+        return torch.empty(shape, dtype=_f32, device=device) if new else None
+    if not _good(x, shape, _f32, device):
+        B, H, K, V = shape
+        _state_arg(x, B, H, K, device, name, V)
+    return x
 
 
-def _scale(scale, K):
-    return ctypes.c_float(K ** -0.5 if scale is None else float(scale))
+def _output(x, shape, device, name, dtype=_f32, dtypes=F32):
+    """An output argument, or a fresh tensor in the place of None."""
+    if x is None:
+        x = torch.empty(shape, dtype=dtype, device=device)
+    return _out_arg(x, shape, device, name, dtypes)
+
+
+BOTH = (torch.float32, torch.bfloat16)
 
 
 def gdr_forward(q, k, v, g, beta, state_in=None, *, scale=None, o_dtype=torch.float32, o=None, state_out=None,
@@ -89,16 +115,15 @@ def gdr_forward(q, k, v, g, beta, state_in=None, *, scale=None, o_dtype=torch.fl
     to [0, T]); o[b, t] for t >= lengths[b] is left as it was.
     """
     B, T, Hk, H, K, V, dev = _check_inputs(q, k, v, g, beta)
-    state_in = _state_arg(state_in, B, H, K, dev, "state_in", V)
-    state_out = _new((B, H, K, V), dev) if state_out is None else state_out
-    _state_arg(state_out, B, H, K, dev, "state_out", V)
-    o = _new((B, T, H, V), dev, o_dtype) if o is None else o
-    _out_arg(o, (B, T, H, V), dev, "o")
+    shape = (B, H, K, V)
+    state_in = _state(state_in, shape, dev, "state_in")
+    state_out = _state(state_out, shape, dev, "state_out", True)
+    o = _output(o, (B, T, H, V), dev, "o", o_dtype, BOTH)
     with _on(dev):
         lengths = None if lengths is None else _int_rows(lengths, B, dev, "lengths")
-        _check(lib().gdr_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _dt(q), _ptr(state_in), _ptr(o),
-                                 _dt(o), _ptr(state_out), _ptr(lengths), _scale(scale, K), B, T, Hk, H, K, V,
-                                 _stream(dev)))
+        _check(lib().gdr_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _dt(q),
+                                 _p(state_in), o.data_ptr(), _dt(o), state_out.data_ptr(), _p(lengths),
+                                 K ** -0.5 if scale is None else scale, B, T, Hk, H, K, V, _stream(dev)))
     return o, state_out
 
 
@@ -111,23 +136,18 @@ def gdr_step(q, k, v, g, beta, state_in=None, *, scale=None, per_position=False,
     state (state_out is None).
     """
     B, T, Hk, H, K, V, dev = _check_inputs(q, k, v, g, beta)
-    state_in = _state_arg(state_in, B, H, K, dev, "state_in", V)
-    if not write_state_out:
-        if not (per_position or state_pos is not None) or state_out is not None:
-            raise ValueError("write_state_out=False needs per-position states and no state_out")
-    elif state_out is None:
-        state_out = _new((B, H, K, V), dev)
-    _state_arg(state_out, B, H, K, dev, "state_out", V)
-    o = _new((B, T, H, V), dev, o_dtype) if o is None else o
-    _out_arg(o, (B, T, H, V), dev, "o")
-    if per_position and state_pos is None:
-        state_pos = _new((B, T, H, K, V), dev)
-    if state_pos is not None:
-        _out_arg(state_pos, (B, T, H, K, V), dev, "state_pos", F32)
+    shape = (B, H, K, V)
+    state_in = _state(state_in, shape, dev, "state_in")
+    if not write_state_out and (not (per_position or state_pos is not None) or state_out is not None):
+        raise ValueError("write_state_out=False needs per-position states and no state_out")
+    state_out = _state(state_out, shape, dev, "state_out", write_state_out)
+    o = _output(o, (B, T, H, V), dev, "o", o_dtype, BOTH)
+    if per_position or state_pos is not None:
+        state_pos = _output(state_pos, (B, T, H, K, V), dev, "state_pos")
     with _on(dev):
-        _check(lib().gdr_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _dt(q), _ptr(state_in), _ptr(o),
-                              _dt(o), _ptr(state_out), _ptr(state_pos), _scale(scale, K), B, T, Hk, H, K, V,
-                              _stream(dev)))
+        _check(lib().gdr_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _dt(q),
+                              _p(state_in), o.data_ptr(), _dt(o), _p(state_out), _p(state_pos),
+                              K ** -0.5 if scale is None else scale, B, T, Hk, H, K, V, _stream(dev)))
     return (o, state_out) if state_pos is None else (o, state_out, state_pos)
 
 
@@ -144,19 +164,17 @@ def gdr_forward_ckpt(q, k, v, g, beta, state_in=None, *, scale=None, o=None, sta
     gdr_backward_ckpt reads.
     """
     B, T, Hk, H, K, V, dev = _check_inputs(q, k, v, g, beta)
-    state_in = _state_arg(state_in, B, H, K, dev, "state_in", V)
-    state_out = _new((B, H, K, V), dev) if state_out is None else state_out
-    _state_arg(state_out, B, H, K, dev, "state_out", V)
-    o = _new((B, T, H, V), dev) if o is None else o
-    _out_arg(o, (B, T, H, V), dev, "o", F32)
-    ckpt = _new((B, _nblocks(T), H, K * V), dev) if ckpt is None else ckpt
-    _out_arg(ckpt, (B, _nblocks(T), H, K * V), dev, "ckpt", F32)
-    resid = _new((B, T, H, V), dev) if resid is None else resid
-    _out_arg(resid, (B, T, H, V), dev, "resid", F32)
+    shape = (B, H, K, V)
+    state_in = _state(state_in, shape, dev, "state_in")
+    state_out = _state(state_out, shape, dev, "state_out", True)
+    o = _output(o, (B, T, H, V), dev, "o")
+    ckpt = _output(ckpt, (B, _nblocks(T), H, K * V), dev, "ckpt")
+    resid = _output(resid, (B, T, H, V), dev, "resid")
     with _on(dev):
-        _check(lib().gdr_forward_ckpt(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _dt(q), _ptr(state_in),
-                                      _ptr(o), _ptr(state_out), _ptr(ckpt) if T else None,
-                                      _ptr(resid) if T else None, _scale(scale, K), B, T, Hk, H, K, V, _stream(dev)))
+        _check(lib().gdr_forward_ckpt(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _dt(q),
+                                      _p(state_in), o.data_ptr(), state_out.data_ptr(), ckpt.data_ptr(),
+                                      resid.data_ptr(), K ** -0.5 if scale is None else scale, B, T, Hk, H, K, V,
+                                      _stream(dev)))
     return o, state_out, ckpt, resid
 
 
@@ -173,19 +191,19 @@ def gdr_backward_ckpt(q, k, g, beta, ckpt, resid, d_o, d_state_out=None, *, scal
     H, V = d_o.shape[2:]
     B, T, Hk, K, dev = _check_qk(q, k, g, beta, H)
     _out_arg(d_o, (B, T, H, V), dev, "d_o", F32)
-    d_state_out = _state_arg(d_state_out, B, H, K, dev, "d_state_out", V)
-    _out_arg(ckpt, (B, _nblocks(T), H, K * V), dev, "ckpt", F32)
+    d_state_out = _state(d_state_out, (B, H, K, V), dev, "d_state_out")
+    saved = (B, _nblocks(T), H, K * V)
+    _out_arg(ckpt, saved, dev, "ckpt", F32)
     _out_arg(resid, (B, T, H, V), dev, "resid", F32)
     shapes = {"dq": (B, T, Hk, K), "dk": (B, T, Hk, K), "dv": (B, T, H, V), "dg": (B, T, H), "dbeta": (B, T, H),
               "d_state_in": (B, H, K, V)}
     if grads is None:
-        grads = {n: _new(s, dev) for n, s in shapes.items()}
-    for n, s in shapes.items():
-        _out_arg(grads[n], s, dev, n, F32)
-    work = _new((B, _nblocks(T), H, K * V), dev) if work is None else work
-    _out_arg(work, (B, _nblocks(T), H, K * V), dev, "work", F32)
+        grads = dict.fromkeys(shapes)
+    grads = {n: _output(grads[n], s, dev, n) for n, s in shapes.items()}
+    work = _output(work, saved, dev, "work")
     with _on(dev):
-        _check(lib().gdr_backward_ckpt(_ptr(q), _ptr(k), _ptr(g), _ptr(beta), _dt(q), *[_ptr(x) if T else None for x in (ckpt, resid, d_o)],
-                                       _ptr(d_state_out), *[_ptr(grads[n]) for n in shapes],
-                                       _ptr(work) if T else None, _scale(scale, K), B, T, Hk, H, K, V, _stream(dev)))
+        _check(lib().gdr_backward_ckpt(q.data_ptr(), k.data_ptr(), g.data_ptr(), beta.data_ptr(), _dt(q),
+                                       ckpt.data_ptr(), resid.data_ptr(), d_o.data_ptr(), _p(d_state_out),
+                                       *[grads[n].data_ptr() for n in shapes], work.data_ptr(),
+                                       K ** -0.5 if scale is None else scale, B, T, Hk, H, K, V, _stream(dev)))
     return grads
