@@ -36,7 +36,8 @@
 // Q carries a power of two that brings its largest entry into [1/2, 1); a column of the state
 // is kept in registers multiplied by a power of two (up), which changes only when the column
 // leaves [2^-2, 2^13] or an added term 2^8: 32 terms below 2^8 then stay below the fp16
-// limit of 65504.  The 32 x 32 products run on three bf16 pieces (A R on two where o is bf16,
+// limit of 65504.  (Rows of norms in [1/8, 2], as normalised keys are, go without a power:
+// their squares are on the diagonal of K K^T.)  The 32 x 32 products run on three bf16 pieces (A R on two where o is bf16,
 // whose own rounding is 2^-8); the unit diagonal of the inverse is added in fp32.
 #include <type_traits>
 
@@ -71,16 +72,20 @@ template <typename Tin> constexpr int input_pieces_b() { return std::is_same<Tin
 
 template <int K, int NP, int NA>
 struct Smem {
-    uint16_t k[2][NP][C][K + 16], q[2][NP][C][K + 16];
+    alignas(16) uint16_t k[2][NP][C][K + 16];
+    alignas(16) uint16_t q[2][NP][C][K + 16];
     // inverse - I and A as [row][token slot] (backward: transposed); token t < 16 has slot
     // 8 (t/4) + t%4, token 16 + t four more: a fragment's eight tokens are consecutive
-    uint16_t t[2][3][C][LDT], a[2][NA][C][LDT];
-    float x[2][C][36];         // x[j][i] = the triangular matrix at (i, j)
-    float p[2][C][34];         // P; column 32: gamma (33: not used)
-    float d[2][16][20];        // the inverse's diagonal blocks
-    float vec[4][4][C];        // gamma | beta P_C (backward: P_C) | beta | gamma beta
-    float con[4][3][C];        // vec 0, 1 (backward: 1, -3) with K's row factors; scale gamma with Q's
-    float kf[C], qf[C];        // row factors: K's (K wave), Q's (Q wave)
+    alignas(16) uint16_t t[2][3][C][LDT];
+    alignas(16) uint16_t a[2][NA][C][LDT];
+    alignas(16) float x[2][C][36];   // x[j][i] = the triangular matrix at (i, j)
+    alignas(16) float d[2][16][20];  // the inverse's diagonal blocks, [column][row]
+    alignas(16) float vec[4][4][C];  // gamma | beta P_C (backward: P_C) | beta | gamma beta
+    alignas(16) float con[4][3][C];  // vec 0, 1 (backward: 1, -3) with K's row factors; scale gamma with Q's
+    float kf[C], qf[C];              // row factors: K's (K wave), Q's (Q wave)
+    alignas(16) float head[2][C];    // P from the start of a token's half chunk to the token
+    alignas(16) float tail[2][C];    // P from behind the token to the end of its half
+    float p[2][2][16][17];           // P inside the halves
 };
 
 // Eight input elements of a row.
@@ -97,6 +102,11 @@ template <> struct Raw<uint16_t> {
         for (int e = 1; e < 4; ++e)
             m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, x[e] & 0x7fff7fffu));
         return static_cast<uint32_t>(m[0] > m[1] ? m[0] : m[1]) << 16;
+    }
+    __device__ void planes(float m1, s16x8 (&out)[1]) const
+    {
+        split8h<1>(f32x4{bf16_lo(x[0]), bf16_hi(x[0]), bf16_lo(x[1]), bf16_hi(x[1])},
+                   f32x4{bf16_lo(x[2]), bf16_hi(x[2]), bf16_lo(x[3]), bf16_hi(x[3])}, out, m1);
     }
     __device__ void planes(float f, float m1, s16x8 (&out)[1]) const
     {
@@ -121,6 +131,7 @@ template <> struct Raw<float> {
             m = max(m, max(__float_as_uint(x[e]) & 0x7fffffffu, __float_as_uint(y[e]) & 0x7fffffffu));
         return m;
     }
+    __device__ void planes(float m1, s16x8 (&out)[2]) const { split8h<2>(x, y, out, m1); }
     __device__ void planes(float f, float m1, s16x8 (&out)[2]) const { split8h<2>(x * f, y * f, out, m1); }
     __device__ void bf16(s16x8 (&out)[3]) const { split8<3>(x, y, out); }
     __device__ void clear() { x = y = f32x4{0.f, 0.f, 0.f, 0.f}; }
@@ -135,17 +146,29 @@ __device__ __forceinline__ int exponent(uint32_t bits)
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-// Two rows' elements of one column.
-__device__ __forceinline__ void put2(float *p, unsigned at, unsigned stride, float x, float y)
+// The element `bytes` behind a base that is the same for the whole wave: one 32-bit offset a lane.
+template <typename T>
+__device__ __forceinline__ T &lane_at(T *p, unsigned bytes)
 {
-    p[at] = x;
-    (p + stride)[at] = y;
+    return *reinterpret_cast<T *>(reinterpret_cast<char *>(p) + bytes);
 }
-__device__ __forceinline__ void put2(uint16_t *p, unsigned at, unsigned stride, float x, float y)
+template <typename T>
+__device__ __forceinline__ const T &lane_at(const T *p, unsigned bytes)
+{
+    return *reinterpret_cast<const T *>(reinterpret_cast<const char *>(p) + bytes);
+}
+
+// Two elements, each to an address of its own.
+__device__ __forceinline__ void put2(float &a, float &b, float x, float y)
+{
+    a = x;
+    b = y;
+}
+__device__ __forceinline__ void put2(uint16_t &a, uint16_t &b, float x, float y)
 {
     const uint32_t u = pk_bf16(x, y);
-    p[at] = static_cast<uint16_t>(u);
-    (p + stride)[at] = static_cast<uint16_t>(u >> 16);
+    a = static_cast<uint16_t>(u);
+    b = static_cast<uint16_t>(u >> 16);
 }
 
 // What every wave of a workgroup knows.
@@ -156,37 +179,57 @@ struct Place {
     size_t tok0;
 };
 
-// Decays of chunk s + 3: lane j < 32 walks down column j of P, lane 32 down gamma.
+// x of lane `J` of this lane's row of 16.
+template <int J>
+__device__ __forceinline__ float row_lane(float x)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + J, 0xf, 0xf, true));
+}
+
+// Walk down the columns of a half's decays: lane (half, row) holds alpha of its token; on
+// return p = P(last, row), all the product of all and from = that up to the token.
+template <int I>
+__device__ __forceinline__ void walk(float alpha, int row, float &p, float &all, float &from, float (*out)[17])
+{
+    if constexpr (I < 16) {
+        const float x = row_lane<I>(alpha), next = p * x;
+        const bool here = I == row;
+        all *= x;
+        p = here ? 1.f : next;
+        from = here ? all : from;
+        out[I][row] = p;
+        walk<I + 1>(alpha, row, p, all, from, out);
+    }
+}
+
+// Decays of chunk s + 3.
 template <bool BACK, typename SM>
 __device__ __forceinline__ void decay_wave(SM &sm, const ChainArgs &a, const Place &w)
 {
     float g[2], be[2];
     auto load = [&](int s, int at) {
-        const int c = BACK ? w.n - 1 - s : s, t = c * C + w.lane;
+        const int c = BACK ? w.n - 1 - s : s, t = c * C + (w.lane & (C - 1));
         g[at] = be[at] = 0.f;  // behind the end: no decay, nothing written
-        if (s < w.n && w.lane < C && t < w.L) {
+        if (s < w.n && t < w.L) {
             const size_t i = (w.tok0 + t) * a.H + w.h;
             g[at] = a.g[i];
             be[at] = a.beta[i];
         }
     };
-    const int col = min(w.lane, C + 1);
     auto body = [&](int s, auto at) {
         if (s < w.n) {
             const float alpha = expf(g[at]), beta = be[at];
             load(s + 2, at);
-            float p = w.lane == C ? 1.f : 0.f;
-#pragma unroll
-            for (int i = 0; i < C; ++i) {
-                const float next = p * wkv7::lane_bcast(alpha, i);
-                p = i == w.lane ? 1.f : next;
-                sm.p[s & 1][i][col] = p;
-            }
-            wave_lds_fence();
+            const int half = w.quad & 1;  // the upper 32 lanes repeat the lower
+            float tail = 0.f, all = 1.f, from = 0.f;
+            walk<0>(alpha, w.row, tail, all, from, sm.p[s & 1][half]);
+            const float first = wkv7::lane_bcast(all, 0), second = wkv7::lane_bcast(all, 16);
+            const float gamma = half ? first * from : from, toend = half ? tail : tail * second;
             if (w.lane < C) {
-                const float gamma = sm.p[s & 1][w.lane][C];
+                sm.head[s & 1][w.lane] = from;
+                sm.tail[s & 1][w.lane] = tail;
                 sm.vec[s & 3][0][w.lane] = gamma;
-                sm.vec[s & 3][1][w.lane] = BACK ? p : p * beta;
+                sm.vec[s & 3][1][w.lane] = BACK ? toend : toend * beta;
                 sm.vec[s & 3][2][w.lane] = beta;
                 sm.vec[s & 3][3][w.lane] = gamma * beta;
             }
@@ -205,23 +248,21 @@ __device__ __forceinline__ void decay_wave(SM &sm, const ChainArgs &a, const Pla
     }
 }
 
-// x of lane `J` of this lane's row of 16.
-template <int J>
-__device__ __forceinline__ float row_lane(float x)
-{
-    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + J, 0xf, 0xf, true));
-}
-
 // One step of the substitution: c[i] -= M(i, J) c[J] for i > J, then the next.  Lane (column
-// of the inverse) r of a row of 16 holds M(i, r) in m[i].
+// of the inverse) r of a row of 16 holds M(i, r) in m[i]; the broadcast of lane J's is part of
+// the multiply-add.  (m must not have been written by the vector unit in the two cycles before:
+// the s_nop.)
 template <int J>
 __device__ __forceinline__ void eliminate(float (&c)[16], const float (&m)[16])
 {
     if constexpr (J < 15) {
         const float x = -c[J];
+        asm volatile("s_nop 1");
 #pragma unroll
         for (int i = J + 1; i < 16; ++i)
-            c[i] = fmaf(row_lane<J>(m[i]), x, c[i]);
+            asm volatile("v_fmac_f32_dpp %0, %1, %2 row_newbcast:%3 row_mask:0xf bank_mask:0xf"
+                         : "+v"(c[i])
+                         : "v"(m[i]), "v"(x), "n"(J));
         eliminate<J + 1>(c, m);
     }
 }
@@ -231,6 +272,12 @@ template <bool BACK, typename SM>
 __device__ __forceinline__ void inverse_wave(SM &sm, const Place &w)
 {
     const int row = w.row, quad = w.quad, blk = quad & 1;
+    float unit[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        unit[i] = i == row ? 1.f : 0.f;
+        asm volatile("" : "+v"(unit[i]));  // kept in a register: 16 lane masks would not be
+    }
     for (int it = -3; it < w.n; ++it) {
         const int s = it + 1;
         if (s >= 0 && s < w.n) {
@@ -243,7 +290,7 @@ __device__ __forceinline__ void inverse_wave(SM &sm, const Place &w)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     m[i + e] = u[e];
-                    c[i + e] = i + e == row ? 1.f : 0.f;
+                    c[i + e] = unit[i + e];
                 }
             }
             // the block below, read ahead
@@ -254,36 +301,48 @@ __device__ __forceinline__ void inverse_wave(SM &sm, const Place &w)
             eliminate<0>(c, m);
             if (w.lane < 32)
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    sm.d[blk][i][row] = c[i];
+                for (int i = 0; i < 16; i += 4)
+                    *reinterpret_cast<f32x4 *>(&sm.d[blk][row][i]) = f32x4{c[i], c[i + 1], c[i + 2], c[i + 3]};
             wave_lds_fence();
             // the block below the diagonal, -D1 M D0 (backward: its rows; forward: transposed)
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f}, below = acc;
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f}, below = acc, right, diag[2];
+            float left[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int u = 4 * e + quad;
-                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(low[e], BACK ? sm.d[0][u][row] : sm.d[1][row][u], acc, 0, 0, 0);
+            for (int e = 0; e < 4; ++e)
+                left[e] = BACK ? sm.d[0][row][4 * e + quad] : sm.d[1][4 * e + quad][row];
+            if constexpr (BACK) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    right[e] = sm.d[1][4 * quad + e][row];
+                diag[0] = *reinterpret_cast<const f32x4 *>(&sm.d[0][row][4 * quad]);
+                diag[1] = *reinterpret_cast<const f32x4 *>(&sm.d[1][row][4 * quad]);
+            } else {
+                right = *reinterpret_cast<const f32x4 *>(&sm.d[0][row][4 * quad]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    diag[0][e] = sm.d[0][4 * quad + e][row];
+                    diag[1][e] = sm.d[1][4 * quad + e][row];
+                }
             }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(low[e], left[e], acc, 0, 0, 0);
             u32x2 out[3];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                f32x4 dd;
+                f32x4 dd = diag[e];
 #pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    dd[f] = BACK ? sm.d[e][4 * quad + f][row] : sm.d[e][row][4 * quad + f];
+                for (int f = 0; f < 4; ++f)
                     dd[f] = 4 * quad + f == row ? 0.f : dd[f];
-                }
                 split4<3>(dd, out);
 #pragma unroll
                 for (int p = 0; p < 3; ++p)
                     *reinterpret_cast<u32x2 *>(&sm.t[s & 1][p][16 * e + row][8 * quad + 4 * e]) = out[p];
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int u = 4 * quad + e;
-                below = __builtin_amdgcn_mfma_f32_16x16x4f32(BACK ? sm.d[1][row][u] : sm.d[0][u][row], -acc[e], below, 0,
-                                                             0, 0);
-            }
+            for (int e = 0; e < 4; ++e)
+                below = __builtin_amdgcn_mfma_f32_16x16x4f32(right[e], -acc[e], below, 0, 0, 0);
             split4<3>(below, out);
 #pragma unroll
             for (int p = 0; p < 3; ++p)
@@ -303,21 +362,40 @@ __device__ __forceinline__ void rows_wave(SM &sm, const ChainArgs &a, const Plac
     const int row = w.row, quad = w.quad;
     const float m1 = minus_one();
     const size_t stride = static_cast<size_t>(a.Hk) * K;
-    const Tin *kp = static_cast<const Tin *>(a.k) + (w.tok0 * a.Hk + w.kh) * K + 8 * quad;
-    const Tin *qp = static_cast<const Tin *>(a.q) + (w.tok0 * a.Hk + w.kh) * K + 8 * quad;
+    // [b, 0, kh, 0] and this lane's place in the rows of a tile
+    const Tin *kp = static_cast<const Tin *>(a.k) + (w.tok0 * a.Hk + w.kh) * K;
+    const Tin *qp = static_cast<const Tin *>(a.q) + (w.tok0 * a.Hk + w.kh) * K;
+    const unsigned at0 = static_cast<unsigned>((row * stride + 8 * quad) * sizeof(Tin));
     auto chunk = [&](int s) { return BACK ? w.n - 1 - s : s; };
-    Raw<Tin> kr[DEPTH][2][NM], qr[IS_Q ? DEPTH : 1][2][NM];
-    auto load = [&](int s, int at) {
+    // The Q wave asks for K one chunk ahead only: the K wave has brought those rows to the L2.
+    constexpr int KDEPTH = IS_Q ? 1 : DEPTH;
+    Raw<Tin> kr[KDEPTH][2][NM], qr[IS_Q ? DEPTH : 1][2][NM];
+    auto load = [&](int s, int at, bool of_k, bool of_q) {
         if (s >= w.n)
             return;
+        const int first = chunk(s) * C;
+        const Tin *k = kp + first * stride, *q = qp + first * stride;
+        if (first + C <= w.L) {
 #pragma unroll
-        for (int tau = 0; tau < 2; ++tau) {
-            const int t = min(chunk(s) * C + 16 * tau + row, w.L - 1);
+            for (int tau = 0; tau < 2; ++tau)
 #pragma unroll
-            for (int m = 0; m < NM; ++m) {
-                kr[at][tau][m].load(kp + t * stride + 32 * m);
-                if constexpr (IS_Q)
-                    qr[at][tau][m].load(qp + t * stride + 32 * m);
+                for (int m = 0; m < NM; ++m) {
+                    if (of_k)
+                        kr[IS_Q ? 0 : at][tau][m].load(&lane_at(k + 16 * tau * stride + 32 * m, at0));
+                    if (IS_Q && of_q)
+                        qr[IS_Q ? at : 0][tau][m].load(&lane_at(q + 16 * tau * stride + 32 * m, at0));
+                }
+        } else {  // rows behind the end: the last one again, cleared before use
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau) {
+                const size_t t = min(16 * tau + row, w.L - 1 - first) * stride + 8 * quad;
+#pragma unroll
+                for (int m = 0; m < NM; ++m) {
+                    if (of_k)
+                        kr[IS_Q ? 0 : at][tau][m].load(k + t + 32 * m);
+                    if (IS_Q && of_q)
+                        qr[IS_Q ? at : 0][tau][m].load(q + t + 32 * m);
+                }
             }
         }
     };
@@ -361,17 +439,18 @@ __device__ __forceinline__ void rows_wave(SM &sm, const ChainArgs &a, const Plac
         }
         if (s >= 0 && s < w.n) {
             const int t0 = chunk(s) * C + row;
-            f32x4 acc[3];
+            f32x4 acc[3], self[2];  // self: Q Q^T's diagonal tiles (Q wave)
 #pragma unroll
             for (int e = 0; e < 3; ++e)
                 acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+            self[0] = self[1] = acc[0];
             if (chunk(s) * C + C > w.L)
 #pragma unroll
                 for (int tau = 0; tau < 2; ++tau)
                     if (t0 + 16 * tau >= w.L)
 #pragma unroll
                         for (int m = 0; m < NM; ++m) {
-                            kr[at][tau][m].clear();
+                            kr[IS_Q ? 0 : static_cast<int>(at)][tau][m].clear();
                             if constexpr (IS_Q)
                                 qr[at][tau][m].clear();
                         }
@@ -382,7 +461,7 @@ __device__ __forceinline__ void rows_wave(SM &sm, const ChainArgs &a, const Plac
                 s16x8 kb[2][NB], qb[2][NB];
 #pragma unroll
                 for (int tau = 0; tau < 2; ++tau) {
-                    kr[at][tau][m].bf16(kb[tau]);
+                    kr[IS_Q ? 0 : static_cast<int>(at)][tau][m].bf16(kb[tau]);
                     if constexpr (IS_Q)
                         qr[at][tau][m].bf16(qb[tau]);
                 }
@@ -396,20 +475,51 @@ __device__ __forceinline__ void rows_wave(SM &sm, const ChainArgs &a, const Plac
                     else
                         mma<NB, NB>(acc[e], kb[tj], qb[ti]);
                 }
+                if constexpr (IS_Q)
+#pragma unroll
+                    for (int tau = 0; tau < 2; ++tau)
+                        mma<NB, NB>(self[tau], qb[tau], qb[tau]);
             }
+            if constexpr (!IS_Q) {
+                self[0] = acc[0];
+                self[1] = acc[2];
+            }
+            if (IS_Q)
+                load(s + 1, 0, true, false);
+            // |x|^2 of this lane's rows, from the lanes that hold the diagonal
+            bool plain = true;
 #pragma unroll
             for (int tau = 0; tau < 2; ++tau) {
-                float f;
-                if constexpr (IS_Q)
-                    f = convert(qr[at][tau], held[tau]);
-                else
-                    f = convert(kr[at][tau], held[tau]);
-                if (quad == 0)
-                    (IS_Q ? sm.qf : sm.kf)[16 * tau + row] = f;
+                const f32x4 &d = self[tau];
+                const float lo = row & 1 ? d[1] : d[0], hi = row & 1 ? d[3] : d[2];
+                const float sq = __shfl(row & 2 ? hi : lo, 16 * (row >> 2) + row);
+                plain = plain && ((sq >= 0x1p-6f && sq <= 4.f) || sq == 0.f);
             }
-            load(s + DEPTH, at);
+            float fac[2] = {1.f, 1.f};
+            if (__all(plain)) {  // rows of norms in [1/8, 2]: fp16 holds them as they are
+#pragma unroll
+                for (int tau = 0; tau < 2; ++tau)
+#pragma unroll
+                    for (int m = 0; m < NM; ++m)
+                        if constexpr (IS_Q)
+                            qr[at][tau][m].planes(m1, held[tau][m]);
+                        else
+                            kr[IS_Q ? 0 : static_cast<int>(at)][tau][m].planes(m1, held[tau][m]);
+            } else {
+#pragma unroll
+                for (int tau = 0; tau < 2; ++tau)
+                    if constexpr (IS_Q)
+                        fac[tau] = convert(qr[at][tau], held[tau]);
+                    else
+                        fac[tau] = convert(kr[IS_Q ? 0 : static_cast<int>(at)][tau], held[tau]);
+            }
+            if (quad == 0)
+#pragma unroll
+                for (int tau = 0; tau < 2; ++tau)
+                    (IS_Q ? sm.qf : sm.kf)[16 * tau + row] = fac[tau];
+            load(s + DEPTH, at, !IS_Q, IS_Q);
             wave_lds_fence();
-            const float(*P)[34] = sm.p[s & 1];
+            const float *head = sm.head[s & 1], *tail = sm.tail[s & 1];
             const float *beta = sm.vec[s & 3][2];
             if (w.lane < C) {
                 const int l = w.lane;
@@ -426,20 +536,31 @@ __device__ __forceinline__ void rows_wave(SM &sm, const ChainArgs &a, const Plac
                 f32x4 v;
                 if constexpr (IS_Q && !BACK) {
                     const int i = 16 * ti + row, j0 = 16 * tj + 4 * quad;
-                    const f32x4 be = *reinterpret_cast<const f32x4 *>(&beta[j0]);
+                    const f32x4 x = (a.scale * *reinterpret_cast<const f32x4 *>(&beta[j0])) * acc[e];
+                    if (e == 1) {
+                        v = x * (head[i] * *reinterpret_cast<const f32x4 *>(&tail[j0]));
+                    } else {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float y = P[i][j0 + r] * be[r] * (acc[e][r] * a.scale);
-                        v[r] = j0 + r <= i ? y : 0.f;
+                        for (int r = 0; r < 4; ++r) {
+                            const float y = sm.p[s & 1][ti][row][4 * quad + r] * x[r];
+                            v[r] = 4 * quad + r <= row ? y : 0.f;
+                        }
                     }
                 } else {
                     const int i0 = 16 * ti + 4 * quad, j = 16 * tj + row;
-                    const f32x4 be = *reinterpret_cast<const f32x4 *>(&beta[i0]);
-                    const float bj = beta[j];
+                    f32x4 x;
+                    if constexpr (!IS_Q && BACK)
+                        x = *reinterpret_cast<const f32x4 *>(&beta[i0]) * acc[e];
+                    else
+                        x = (IS_Q ? a.scale : beta[j]) * acc[e];
+                    if (e == 1) {
+                        v = x * (tail[j] * *reinterpret_cast<const f32x4 *>(&head[i0]));
+                    } else {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float y = P[i0 + r][j] * (IS_Q ? a.scale : BACK ? be[r] : bj) * acc[e][r];
-                        v[r] = (IS_Q ? j <= i0 + r : j < i0 + r) ? y : 0.f;
+                        for (int r = 0; r < 4; ++r) {
+                            const float y = sm.p[s & 1][ti][4 * quad + r][row] * x[r];
+                            v[r] = (IS_Q ? row <= 4 * quad + r : row < 4 * quad + r) ? y : 0.f;
+                        }
                     }
                 }
                 if constexpr (IS_Q)
@@ -452,7 +573,9 @@ __device__ __forceinline__ void rows_wave(SM &sm, const ChainArgs &a, const Plac
     };
 #pragma unroll
     for (int i = 0; i < DEPTH; ++i)
-        load(i, i);
+        load(i, i, !IS_Q, IS_Q);
+    if (IS_Q)
+        load(0, 0, true, false);
     // the buffer in use alternates from chunk 0, which iteration -2 takes
     for (int it = -3;;) {
         body(it, std::integral_constant<int, DEPTH - 1>{});
@@ -516,11 +639,14 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
     const size_t vs = static_cast<size_t>(a.H) * a.V;
     // [b, 0, h, 0] of v, o, resid, d_o, and this lane's place in the rows of a chunk
     const size_t row0 = (w.tok0 * a.H + w.h) * a.V;
-    const unsigned at0 = static_cast<unsigned>(4 * quad * vs + col), vs4 = static_cast<unsigned>(vs);
+    unsigned at[4];  // elements; bytes once multiplied by their size
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        at[r] = static_cast<unsigned>((4 * quad + r) * vs + col);
     const size_t st0 = static_cast<size_t>(head) * K * a.V + col;  // [b, h, 0, col] of a state
     auto channel = [&](int t, int r) { return 32 * (t >> 1) + 8 * quad + 4 * (t & 1) + r; };
     using Trow = typename std::conditional<BACK, float, Tin>::type;
-    const Trow *in = static_cast<const Trow *>(BACK ? static_cast<const void *>(a.d_o) : a.v) + row0;  // + at0: this lane's rows
+    const Trow *in = static_cast<const Trow *>(BACK ? static_cast<const void *>(a.d_o) : a.v) + row0;
 
     f32x4 S[NT];  // the state (backward: its gradient) times up
 #pragma unroll
@@ -530,21 +656,20 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
             S[t][r] = a.first ? a.first[st0 + static_cast<size_t>(channel(t, r)) * a.V] : 0.f;
     float up = 1.f, down = 1.f;  // 2^e and 2^-e, one e for each column
     int scale_e = 0;
-    // Bring the column's scale back if an entry of S or an added term (at most `term`) asks for
-    // it.  A column's entries and terms sit in four lanes: too large in one of them, or too
-    // small in all four, is seen in the lanes' votes; maxima are formed only then.
-    auto rescale = [&](float term) -> float {
-        float top = 0.f;
+    // Bring the column's scale back if an entry of S (ask = entries) or an added term asks for it.
+    // A column's entries and terms sit in four lanes: too large in one of them, or too small in
+    // all four, is seen in the lanes' votes; maxima are formed only then.  Returns what the
+    // column was multiplied by.
+    auto largest_entry = [&]() {
+        float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int r = 0; r < 4; r += 2)
-                top = fmaxf(fmaxf(fabsf(S[t][r]), fabsf(S[t][r + 1])), top);
-        unsigned long long big = __ballot(top >= 0x1p-2f);
-        big |= big >> 32;
-        big |= big >> 16;
-        if ((big & 0xffffu) == 0xffffu && !__any(!(top <= 0x1p13f) || !(term <= 0x1p8f)))
-            return 1.f;
+                top[t & 3] = fmaxf(fmaxf(fabsf(S[t][r]), fabsf(S[t][r + 1])), top[t & 3]);
+        return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    };
+    auto rescale = [&](float top, float term) -> float {
         top = __uint_as_float(quad_max(__float_as_uint(top)));
         term = __uint_as_float(quad_max(__float_as_uint(term)));
         const float all = fmaxf(top, 0.125f * term);
@@ -561,7 +686,32 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
             S[t] *= f;
         return f;
     };
-    rescale(0.f);
+    auto check_entries = [&]() {
+        const float top = largest_entry();
+        unsigned long long big = __ballot(top >= 0x1p-2f);
+        big |= big >> 32;
+        big |= big >> 16;
+        if ((big & 0xffffu) != 0xffffu || __any(!(top <= 0x1p13f)))
+            rescale(top, 0.f);
+    };
+    // the terms of a chunk, about to be added
+    auto check_terms = [&](f32x4(&x)[2], f32x4(&y)[2]) {
+        float term = 0.f;
+#pragma unroll
+        for (int tau = 0; tau < 2; ++tau)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                term = fmaxf(fmaxf(fabsf(x[tau][r]), fabsf(y[tau][r])), term);
+        if (__any(!(term <= 0x1p8f))) {
+            const float f = rescale(largest_entry(), term);
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau) {
+                x[tau] *= f;
+                if (BACK)
+                    y[tau] *= f;
+            }
+        }
+    };
 
     Trow next[2][4];
     auto load = [&](int s) {
@@ -572,31 +722,35 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
             for (int tau = 0; tau < 2; ++tau)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    next[tau][r] = (p + (16 * tau + r) * vs)[at0];
+                    next[tau][r] = lane_at(p + 16 * tau * vs, at[r] * static_cast<unsigned>(sizeof(Trow)));
         } else {
 #pragma unroll
             for (int tau = 0; tau < 2; ++tau)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    next[tau][r] = first + 16 * tau + 4 * quad + r < L ? (p + (16 * tau + r) * vs)[at0] : Trow{0};
+                    next[tau][r] = first + 16 * tau + 4 * quad + r < L
+                                       ? lane_at(p + 16 * tau * vs, at[r] * static_cast<unsigned>(sizeof(Trow)))
+                                       : Trow{0};
         }
     };
     // rows of a chunk, to out[t][col]
     auto store = [&](auto *out, int first, const f32x4(&x)[2]) {
         auto *p = out + row0 + first * vs;
+        constexpr unsigned size = sizeof(*out);
         if (first + C <= L) {
 #pragma unroll
             for (int tau = 0; tau < 2; ++tau)
 #pragma unroll
                 for (int r = 0; r < 4; r += 2)
-                    put2(p + (16 * tau + r) * vs, at0, vs4, x[tau][r], x[tau][r + 1]);
+                    put2(lane_at(p + 16 * tau * vs, at[r] * size), lane_at(p + 16 * tau * vs, at[r + 1] * size), x[tau][r],
+                         x[tau][r + 1]);
         } else {
 #pragma unroll
             for (int tau = 0; tau < 2; ++tau)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     if (first + 16 * tau + 4 * quad + r < L)
-                        store_elem(p + (16 * tau + r) * vs, at0, x[tau][r]);
+                        store_elem(&lane_at(p + 16 * tau * vs, at[r] * size), 0, x[tau][r]);
         }
     };
     if (n > 0)
@@ -623,6 +777,8 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
             for (int t = 0; t < NT; ++t)
                 *reinterpret_cast<f32x4 *>(to + 256 * t) = S[t] * down;
         }
+        // Operands are asked for well before the products that use them: a wave alone on its SIMD
+        // has nothing else to hide the LDS behind.
         f32x4 con[3][2];
 #pragma unroll
         for (int x = 0; x < 3; ++x)
@@ -630,48 +786,57 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
             for (int tau = 0; tau < 2; ++tau)
                 con[x][tau] = *reinterpret_cast<const f32x4 *>(&sm.con[s & 3][x][16 * tau + 4 * quad]);
         const float gC = sm.vec[s & 3][0][C - 1];
+        auto rows_of = [&](const uint16_t(&x)[NP][C][K + 16], int m, s16x8(&f)[2][NP]) {
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau)
+#pragma unroll
+                for (int p = 0; p < NP; ++p)
+                    f[tau][p] = lds8(&x[p][16 * tau + row][32 * m + 8 * quad]);
+        };
+        s16x8 kf[NM][2][NP], qf[NM][2][NP];
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+            rows_of(sm.k[slot], m, kf[m]);
+        __builtin_amdgcn_sched_barrier(0);
+        check_entries();
+        if constexpr (!BACK && NP == 1)
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+                rows_of(sm.q[slot], m, qf[m]);
+        __builtin_amdgcn_sched_barrier(0);
 
         // products with the state
         f32x4 ks[2], qs[2];
+        s16x8 Sp[NM][2];
 #pragma unroll
         for (int tau = 0; tau < 2; ++tau)
             ks[tau] = qs[tau] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
-            s16x8 Sp[2];
-            split8h<2>(S[2 * m], S[2 * m + 1], Sp, m1);
-#pragma unroll
-            for (int tau = 0; tau < 2; ++tau) {
-                s16x8 f[NP];
-#pragma unroll
-                for (int p = 0; p < NP; ++p)
-                    f[p] = lds8(&sm.k[slot][p][16 * tau + row][32 * m + 8 * quad]);
-                mmah<NP, 2>(ks[tau], f, Sp);
-                if constexpr (!BACK) {
-#pragma unroll
-                    for (int p = 0; p < NP; ++p)
-                        f[p] = lds8(&sm.q[slot][p][16 * tau + row][32 * m + 8 * quad]);
-                    mmah<NP, 2>(qs[tau], f, Sp);
-                }
-            }
+            split8h<2>(S[2 * m], S[2 * m + 1], Sp[m], m1);
+            mmah2<NP, 2>(ks[0], ks[1], kf[m][0], kf[m][1], Sp[m]);
         }
+        // the 32 x 32 matrices
+        auto matrix = [&](const auto &x, auto &f) {
+            constexpr int NZ = std::extent<std::remove_reference_t<decltype(x)>>::value;
 #pragma unroll
-        for (int tau = 0; tau < 2; ++tau) {
-            ks[tau] *= down;
-            qs[tau] *= down;
-        }
-        // the 32 x 32 matrix x times the rows in zp, on top of out
-        auto apply = [&](const auto &x, const auto &zp, f32x4(&out)[2]) {
-            constexpr int NZ = std::extent<std::remove_reference_t<decltype(zp)>>::value;
-#pragma unroll
-            for (int tau = 0; tau < 2; ++tau) {
-                s16x8 f[NZ];
+            for (int tau = 0; tau < 2; ++tau)
 #pragma unroll
                 for (int p = 0; p < NZ; ++p)
-                    f[p] = lds8(&x[p][16 * tau + row][8 * quad]);
-                mma<NZ, NZ>(out[tau], f, zp);
-            }
+                    f[tau][p] = lds8(&x[p][16 * tau + row][8 * quad]);
         };
+        s16x8 tf[2][3], af[2][NA];
+        matrix(sm.t[slot], tf);
+        if constexpr (BACK)
+            matrix(sm.a[slot], af);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!BACK)
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                if constexpr (NP != 1)
+                    rows_of(sm.q[slot], m, qf[m]);
+                mmah2<NP, 2>(qs[0], qs[1], qf[m][0], qf[m][1], Sp[m]);
+            }
         // K^T or Q^T of state tile t
         auto transposed = [&](const uint16_t(&x)[NP][C][K + 16], int t, s16x8(&f)[NP]) {
             const int at = 32 * (t >> 1) + 8 * (lane & 3) + 4 * (t & 1), r = 4 * quad + (row >> 2);
@@ -679,46 +844,49 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
             for (int p = 0; p < NP; ++p)
                 f[p] = cat(tr4(&x[p][r][at]), tr4(&x[p][16 + r][at]));
         };
-        auto largest = [&](const f32x4(&x)[2], float top) {
-#pragma unroll
-            for (int tau = 0; tau < 2; ++tau)
-#pragma unroll
-                for (int r = 0; r < 4; r += 2)
-                    top = fmaxf(fmaxf(fabsf(x[tau][r]), fabsf(x[tau][r + 1])), top);
-            return top;
-        };
-
         f32x4 R[2], u[2];
         s16x8 zp[3], up2[2];
         if constexpr (!BACK) {
             f32x4 O[2];
+            const float qdown = down;  // qs was formed under this scale
 #pragma unroll
-            for (int tau = 0; tau < 2; ++tau)
+            for (int tau = 0; tau < 2; ++tau) {
+                const f32x4 c = con[0][tau] * down;
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    R[tau][r] = fmaf(-con[0][tau][r], ks[tau][r], v[tau][r]);
+                    R[tau][r] = fmaf(-c[r], ks[tau][r], v[tau][r]);
+            }
             split8<3>(R[0], R[1], zp);
-            apply(sm.t[slot], zp, R);
+            s16x8 kt[NT][NP];
+            if constexpr (NP == 1)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    transposed(sm.k[slot], t, kt[t]);
+            __builtin_amdgcn_sched_barrier(0);
+            mma2<3, 3>(R[0], R[1], tf[0], tf[1], zp);
+            matrix(sm.a[slot], af);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                S[t] *= gC;
 #pragma unroll
             for (int tau = 0; tau < 2; ++tau)
-                u[tau] = con[1][tau] * (R[tau] * up);
-            const float f = rescale(largest(u, 0.f));
-            u[0] *= f;
-            u[1] *= f;
+                u[tau] = (con[1][tau] * up) * R[tau];
+            check_terms(u, u);
             split8h<2>(u[0], u[1], up2, m1);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                s16x8 kt[NP];
-                transposed(sm.k[slot], t, kt);
-                S[t] *= gC;
-                mmah<NP, 2>(S[t], kt, up2);
+            for (int t = 0; t < NT; t += 2) {
+                if constexpr (NP != 1) {
+                    transposed(sm.k[slot], t, kt[t]);
+                    transposed(sm.k[slot], t + 1, kt[t + 1]);
+                }
+                mmah2<NP, 2>(S[t], S[t + 1], kt[t], kt[t + 1], up2);
             }
             s16x8 rp[NA];
             split8<NA>(R[0], R[1], rp);
 #pragma unroll
             for (int tau = 0; tau < 2; ++tau)
-                O[tau] = con[2][tau] * qs[tau];
-            apply(sm.a[slot], rp, O);
+                O[tau] = (con[2][tau] * qdown) * qs[tau];
+            mma2<NA, NA>(O[0], O[1], af[0], af[1], rp);
             store(static_cast<Tout *>(a.o), c * C, O);
             if (MODE == CKPT)
                 store(a.rows, c * C, R);
@@ -728,32 +896,30 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
             split8<3>(v[0], v[1], zp);
 #pragma unroll
             for (int tau = 0; tau < 2; ++tau)
-                R[tau] = con[0][tau] * ks[tau];
-            apply(sm.a[slot], zp, R);
+                R[tau] = (con[0][tau] * down) * ks[tau];
+            mma2<3, 3>(R[0], R[1], af[0], af[1], zp);
             split8<3>(R[0], R[1], zp);
-            apply(sm.t[slot], zp, R);
+            mma2<3, 3>(R[0], R[1], tf[0], tf[1], zp);
 #pragma unroll
             for (int tau = 0; tau < 2; ++tau) {
                 u[tau] = con[1][tau] * (R[tau] * up);
                 y[tau] = con[2][tau] * (v[tau] * up);
             }
             store(a.rows, c * C, R);
-            const float f = rescale(largest(u, largest(y, 0.f)));
-#pragma unroll
-            for (int tau = 0; tau < 2; ++tau) {
-                u[tau] *= f;
-                y[tau] *= f;
-            }
+            check_terms(u, y);
             split8h<2>(u[0], u[1], up2, m1);
             split8h<2>(y[0], y[1], yp, m1);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                s16x8 x[NP];
+            for (int t = 0; t < NT; t += 2) {
+                s16x8 x[2][NP];
                 S[t] *= gC;
-                transposed(sm.q[slot], t, x);
-                mmah<NP, 2>(S[t], x, yp);
-                transposed(sm.k[slot], t, x);
-                mmah<NP, 2>(S[t], x, up2);
+                S[t + 1] *= gC;
+                transposed(sm.q[slot], t, x[0]);
+                transposed(sm.q[slot], t + 1, x[1]);
+                mmah2<NP, 2>(S[t], S[t + 1], x[0], x[1], yp);
+                transposed(sm.k[slot], t, x[0]);
+                transposed(sm.k[slot], t + 1, x[1]);
+                mmah2<NP, 2>(S[t], S[t + 1], x[0], x[1], up2);
             }
         }
         __syncthreads();

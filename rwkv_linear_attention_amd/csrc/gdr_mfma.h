@@ -136,6 +136,43 @@ __device__ __forceinline__ s16x8 cat(const s16x4 a, const s16x4 b)
     return s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
+// Two accumulators at once, with the same right operand: their chains of dependent products
+// alternate.
+template <int NPA, int NPB>
+__device__ __forceinline__ void mma2(f32x4 &acc0, f32x4 &acc1, const s16x8 (&A0)[NPA], const s16x8 (&A1)[NPA],
+                                     const s16x8 (&B)[NPB])
+{
+    constexpr int NPM = NPA > NPB ? NPA : NPB;
+#pragma unroll
+    for (int s = NPM - 1; s >= 0; --s)
+#pragma unroll
+        for (int p = 0; p < NPA; ++p) {
+            const int r = s - p;
+            if (r >= 0 && r < NPB) {
+                const bf16x8 b = __builtin_bit_cast(bf16x8, B[r]);
+                acc0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, A0[p]), b, acc0, 0, 0, 0);
+                acc1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, A1[p]), b, acc1, 0, 0, 0);
+            }
+        }
+}
+template <int NPA, int NPB>
+__device__ __forceinline__ void mmah2(f32x4 &acc0, f32x4 &acc1, const s16x8 (&A0)[NPA], const s16x8 (&A1)[NPA],
+                                      const s16x8 (&B)[NPB])
+{
+    constexpr int NPM = NPA > NPB ? NPA : NPB;
+#pragma unroll
+    for (int s = NPM - 1; s >= 0; --s)
+#pragma unroll
+        for (int p = 0; p < NPA; ++p) {
+            const int r = s - p;
+            if (r >= 0 && r < NPB) {
+                const f16x8 b = __builtin_bit_cast(f16x8, B[r]);
+                acc0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, A0[p]), b, acc0, 0, 0, 0);
+                acc1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, A1[p]), b, acc1, 0, 0, 0);
+            }
+        }
+}
+
 // Maximum over the four lanes that share lane % 16, to all of them.
 __device__ __forceinline__ uint32_t quad_max(uint32_t x)
 {
