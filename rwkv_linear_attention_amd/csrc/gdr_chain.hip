@@ -66,9 +66,8 @@ struct ChainArgs {
     int B, T, Hk, H, V;
 };
 
-// fp16 and bf16 pieces of an input row.
+// fp16 pieces of an input row.
 template <typename Tin> constexpr int input_pieces() { return std::is_same<Tin, float>::value ? 2 : 1; }
-template <typename Tin> constexpr int input_pieces_b() { return std::is_same<Tin, float>::value ? 3 : 1; }
 
 template <int K, int NP, int NA>
 struct Smem {
@@ -82,7 +81,9 @@ struct Smem {
     alignas(16) float d[2][16][20];  // the inverse's diagonal blocks, [column][row]
     alignas(16) float vec[4][4][C];  // gamma | beta P_C (backward: P_C) | beta | gamma beta
     alignas(16) float con[4][3][C];  // vec 0, 1 (backward: 1, -3) with K's row factors; scale gamma with Q's
-    float kf[C], qf[C];              // row factors: K's (K wave), Q's (Q wave)
+    alignas(16) float kf[C];         // row factors: K's (K wave)
+    alignas(16) float qf[C];         // Q's and, with fp32 inputs, K's again (Q wave)
+    alignas(16) float kq[C];
     alignas(16) float head[2][C];    // P from the start of a token's half chunk to the token
     alignas(16) float tail[2][C];    // P from behind the token to the end of its half
     float p[2][2][16][17];           // P inside the halves
@@ -131,9 +132,7 @@ template <> struct Raw<float> {
             m = max(m, max(__float_as_uint(x[e]) & 0x7fffffffu, __float_as_uint(y[e]) & 0x7fffffffu));
         return m;
     }
-    __device__ void planes(float m1, s16x8 (&out)[2]) const { split8h<2>(x, y, out, m1); }
     __device__ void planes(float f, float m1, s16x8 (&out)[2]) const { split8h<2>(x * f, y * f, out, m1); }
-    __device__ void bf16(s16x8 (&out)[3]) const { split8<3>(x, y, out); }
     __device__ void clear() { x = y = f32x4{0.f, 0.f, 0.f, 0.f}; }
 };
 
@@ -357,7 +356,7 @@ __device__ __forceinline__ void inverse_wave(SM &sm, const Place &w)
 template <typename Tin, int K, int NA, bool BACK, bool IS_Q, typename SM>
 __device__ __forceinline__ void rows_wave(SM &sm, const ChainArgs &a, const Place &w)
 {
-    constexpr int NP = input_pieces<Tin>(), NB = input_pieces_b<Tin>(), NM = K / 32;
+    constexpr int NP = input_pieces<Tin>(), NM = K / 32;
     constexpr int DEPTH = std::is_same<Tin, float>::value ? 1 : 2;  // chunks of raw rows in flight
     const int row = w.row, quad = w.quad;
     const float m1 = minus_one();
@@ -456,62 +455,93 @@ __device__ __forceinline__ void rows_wave(SM &sm, const ChainArgs &a, const Plac
                         }
             // lane: column of the tile; registers: rows 4 quad ..  The Q wave's forward tiles
             // are transposed, as A's rows are stored.
+            float fac[2] = {1.f, 1.f}, kfac[2] = {1.f, 1.f};
+            if constexpr (NP == 1) {
 #pragma unroll
-            for (int m = 0; m < NM; ++m) {
-                s16x8 kb[2][NB], qb[2][NB];
+                for (int m = 0; m < NM; ++m) {
+                    s16x8 kb[2][1], qb[2][1];
+#pragma unroll
+                    for (int tau = 0; tau < 2; ++tau) {
+                        kr[IS_Q ? 0 : static_cast<int>(at)][tau][m].bf16(kb[tau]);
+                        if constexpr (IS_Q)
+                            qr[at][tau][m].bf16(qb[tau]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) {
+                        const int ti = e > 0, tj = e > 1;
+                        if constexpr (!IS_Q)
+                            mma<1, 1>(acc[e], kb[ti], kb[tj]);
+                        else if constexpr (BACK)
+                            mma<1, 1>(acc[e], qb[ti], kb[tj]);
+                        else
+                            mma<1, 1>(acc[e], kb[tj], qb[ti]);
+                    }
+                    if constexpr (IS_Q)
+#pragma unroll
+                        for (int tau = 0; tau < 2; ++tau)
+                            mma<1, 1>(self[tau], qb[tau], qb[tau]);
+                }
+                if constexpr (!IS_Q) {
+                    self[0] = acc[0];
+                    self[1] = acc[2];
+                }
+                if (IS_Q)
+                    load(s + 1, 0, true, false);
+                // |x|^2 of this lane's rows, from the lanes that hold the diagonal
+                bool plain = true;
 #pragma unroll
                 for (int tau = 0; tau < 2; ++tau) {
-                    kr[IS_Q ? 0 : static_cast<int>(at)][tau][m].bf16(kb[tau]);
-                    if constexpr (IS_Q)
-                        qr[at][tau][m].bf16(qb[tau]);
+                    const f32x4 &d = self[tau];
+                    const float lo = row & 1 ? d[1] : d[0], hi = row & 1 ? d[3] : d[2];
+                    const float sq = __shfl(row & 2 ? hi : lo, 16 * (row >> 2) + row);
+                    plain = plain && ((sq >= 0x1p-6f && sq <= 4.f) || sq == 0.f);
                 }
-#pragma unroll
-                for (int e = 0; e < 3; ++e) {
-                    const int ti = e > 0, tj = e > 1;
-                    if constexpr (!IS_Q)
-                        mma<NB, NB>(acc[e], kb[ti], kb[tj]);
-                    else if constexpr (BACK)
-                        mma<NB, NB>(acc[e], qb[ti], kb[tj]);
-                    else
-                        mma<NB, NB>(acc[e], kb[tj], qb[ti]);
-                }
-                if constexpr (IS_Q)
+                if (__all(plain)) {  // rows of norms in [1/8, 2]: fp16 holds them as they are
 #pragma unroll
                     for (int tau = 0; tau < 2; ++tau)
-                        mma<NB, NB>(self[tau], qb[tau], qb[tau]);
-            }
-            if constexpr (!IS_Q) {
-                self[0] = acc[0];
-                self[1] = acc[2];
-            }
-            if (IS_Q)
-                load(s + 1, 0, true, false);
-            // |x|^2 of this lane's rows, from the lanes that hold the diagonal
-            bool plain = true;
 #pragma unroll
-            for (int tau = 0; tau < 2; ++tau) {
-                const f32x4 &d = self[tau];
-                const float lo = row & 1 ? d[1] : d[0], hi = row & 1 ? d[3] : d[2];
-                const float sq = __shfl(row & 2 ? hi : lo, 16 * (row >> 2) + row);
-                plain = plain && ((sq >= 0x1p-6f && sq <= 4.f) || sq == 0.f);
-            }
-            float fac[2] = {1.f, 1.f};
-            if (__all(plain)) {  // rows of norms in [1/8, 2]: fp16 holds them as they are
+                        for (int m = 0; m < NM; ++m)
+                            if constexpr (IS_Q)
+                                qr[at][tau][m].planes(m1, held[tau][m]);
+                            else
+                                kr[at][tau][m].planes(m1, held[tau][m]);
+                } else {
 #pragma unroll
-                for (int tau = 0; tau < 2; ++tau)
-#pragma unroll
-                    for (int m = 0; m < NM; ++m)
+                    for (int tau = 0; tau < 2; ++tau)
                         if constexpr (IS_Q)
-                            qr[at][tau][m].planes(m1, held[tau][m]);
+                            fac[tau] = convert(qr[at][tau], held[tau]);
                         else
-                            kr[IS_Q ? 0 : static_cast<int>(at)][tau][m].planes(m1, held[tau][m]);
-            } else {
+                            fac[tau] = convert(kr[at][tau], held[tau]);
+                }
+            } else {  // fp32: the products run on the fp16 pieces too
+                s16x8 kh[2][NM][NP];
 #pragma unroll
-                for (int tau = 0; tau < 2; ++tau)
-                    if constexpr (IS_Q)
-                        fac[tau] = convert(qr[at][tau], held[tau]);
-                    else
-                        fac[tau] = convert(kr[IS_Q ? 0 : static_cast<int>(at)][tau], held[tau]);
+                for (int tau = 0; tau < 2; ++tau) {
+                    if constexpr (IS_Q) {
+                        kfac[tau] = convert(kr[0][tau], kh[tau]);
+                        fac[tau] = convert(qr[0][tau], held[tau]);
+                    } else {
+                        fac[tau] = kfac[tau] = convert(kr[0][tau], held[tau]);
+                    }
+                }
+                if (IS_Q)
+                    load(s + 1, 0, true, false);
+#pragma unroll
+                for (int m = 0; m < NM; ++m)
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) {
+                        const int ti = e > 0, tj = e > 1;
+                        if constexpr (!IS_Q)
+                            mmah<NP, NP>(acc[e], held[ti][m], held[tj][m]);
+                        else if constexpr (BACK)
+                            mmah<NP, NP>(acc[e], held[ti][m], kh[tj][m]);
+                        else
+                            mmah<NP, NP>(acc[e], kh[tj][m], held[ti][m]);
+                    }
+                if (IS_Q && quad == 0)
+#pragma unroll
+                    for (int tau = 0; tau < 2; ++tau)
+                        sm.kq[16 * tau + row] = kfac[tau];
             }
             if (quad == 0)
 #pragma unroll
@@ -519,6 +549,15 @@ __device__ __forceinline__ void rows_wave(SM &sm, const ChainArgs &a, const Plac
                     (IS_Q ? sm.qf : sm.kf)[16 * tau + row] = fac[tau];
             load(s + DEPTH, at, !IS_Q, IS_Q);
             wave_lds_fence();
+            if constexpr (NP != 1)  // the powers of both rows
+#pragma unroll
+                for (int e = 0; e < 3; ++e) {
+                    const int ti = e > 0, tj = e > 1;
+                    if constexpr (IS_Q && !BACK)
+                        acc[e] *= fac[ti] * *reinterpret_cast<const f32x4 *>(&sm.kq[16 * tj + 4 * quad]);
+                    else
+                        acc[e] *= kfac[tj] * *reinterpret_cast<const f32x4 *>(&(IS_Q ? sm.qf : sm.kf)[16 * ti + 4 * quad]);
+                }
             const float *head = sm.head[s & 1], *tail = sm.tail[s & 1];
             const float *beta = sm.vec[s & 3][2];
             if (w.lane < C) {
@@ -810,7 +849,8 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
         __builtin_amdgcn_sched_barrier(0);
         if (MODE == FWD && s > 0)
             store_rows(c - 1);
-        if ((s & 1) == 0)  // twice the most a chunk adds, 2^14, still fits on top of 2^13
+        // a chunk adds at most 2^14 (backward: twice that), which twice over still fits on top of 2^13
+        if (BACK || (s & 1) == 0)
             check_entries();
         if constexpr (!BACK && NP == 1)
 #pragma unroll
