@@ -21,8 +21,8 @@
 // the accumulator layout of the matrix cores, and do the products above; four producer
 // waves prepare what does not depend on the state, up to three chunks ahead:
 //     decay wave  (s + 3)  P, gamma and the vectors derived from them
-//     K wave      (s + 2)  X = P o K K^T;  the rows of K to LDS one chunk later
-//     Q wave      (s + 2)  A = P o Q K^T;  A and the rows of Q to LDS one chunk later
+//     K wave      (s + 2)  the rows of K, X = P o K K^T
+//     Q wave      (s + 1)  the rows of Q, A = P o Q K^T (K from LDS)
 //     inverse     (s + 1)  (I + X B)^-1 - I: two 16 x 16 blocks by substitution in fp32,
 //                          the block below by fp32 matrix products.
 // (Substitution, not products of powers of X: with equal keys the powers grow to 3000 and
@@ -71,7 +71,7 @@ template <typename Tin> constexpr int input_pieces() { return std::is_same<Tin, 
 
 template <int K, int NP, int NA>
 struct Smem {
-    alignas(16) uint16_t k[2][NP][C][K + 16];
+    alignas(16) uint16_t k[3][NP][C][K + 16];
     alignas(16) uint16_t q[2][NP][C][K + 16];
     // inverse - I and A as [row][token slot] (backward: transposed); token t < 16 has slot
     // 8 (t/4) + t%4, token 16 + t four more: a fragment's eight tokens are consecutive
@@ -82,11 +82,11 @@ struct Smem {
     alignas(16) float vec[4][4][C];  // gamma | beta P_C (backward: P_C) | beta | gamma beta
     alignas(16) float con[4][3][C];  // vec 0, 1 (backward: 1, -3) with K's row factors; scale gamma with Q's
     alignas(16) float kf[C];         // row factors: K's (K wave)
-    alignas(16) float qf[C];         // Q's and, with fp32 inputs, K's again (Q wave)
-    alignas(16) float kq[C];
-    alignas(16) float head[2][C];    // P from the start of a token's half chunk to the token
-    alignas(16) float tail[2][C];    // P from behind the token to the end of its half
-    float p[2][2][16][17];           // P inside the halves
+    alignas(16) float qf[C];         // Q's (Q wave)
+    alignas(16) float bk[4][C];      // beta with K's row factors (backward: these alone)
+    alignas(16) float head[4][C];    // P from the start of a token's half chunk to the token
+    alignas(16) float tail[4][C];    // P from behind the token to the end of its half
+    float p[4][2][16][17];           // P inside the halves
 };
 
 // Eight input elements of a row.
@@ -221,12 +221,12 @@ __device__ __forceinline__ void decay_wave(SM &sm, const ChainArgs &a, const Pla
             load(s + 2, at);
             const int half = w.quad & 1;  // the upper 32 lanes repeat the lower
             float tail = 0.f, all = 1.f, from = 0.f;
-            walk<0>(alpha, w.row, tail, all, from, sm.p[s & 1][half]);
+            walk<0>(alpha, w.row, tail, all, from, sm.p[s & 3][half]);
             const float first = wkv7::lane_bcast(all, 0), second = wkv7::lane_bcast(all, 16);
             const float gamma = half ? first * from : from, toend = half ? tail : tail * second;
             if (w.lane < C) {
-                sm.head[s & 1][w.lane] = from;
-                sm.tail[s & 1][w.lane] = tail;
+                sm.head[s & 3][w.lane] = from;
+                sm.tail[s & 3][w.lane] = tail;
                 sm.vec[s & 3][0][w.lane] = gamma;
                 sm.vec[s & 3][1][w.lane] = BACK ? toend : toend * beta;
                 sm.vec[s & 3][2][w.lane] = beta;
@@ -351,276 +351,314 @@ __device__ __forceinline__ void inverse_wave(SM &sm, const Place &w)
     }
 }
 
-// The K wave (IS_Q false) and the Q wave: products of the rows of chunk s + 2; the rows
-// themselves go to LDS one chunk later.
-template <typename Tin, int K, int NA, bool BACK, bool IS_Q, typename SM>
-__device__ __forceinline__ void rows_wave(SM &sm, const ChainArgs &a, const Place &w)
-{
-    constexpr int NP = input_pieces<Tin>(), NM = K / 32;
-    constexpr int DEPTH = std::is_same<Tin, float>::value ? 1 : 2;  // chunks of raw rows in flight
-    const int row = w.row, quad = w.quad;
-    const float m1 = minus_one();
-    const size_t stride = static_cast<size_t>(a.Hk) * K;
-    // [b, 0, kh, 0] and this lane's place in the rows of a tile
-    const Tin *kp = static_cast<const Tin *>(a.k) + (w.tok0 * a.Hk + w.kh) * K;
-    const Tin *qp = static_cast<const Tin *>(a.q) + (w.tok0 * a.Hk + w.kh) * K;
-    const unsigned at0 = static_cast<unsigned>((row * stride + 8 * quad) * sizeof(Tin));
-    auto chunk = [&](int s) { return BACK ? w.n - 1 - s : s; };
-    // The Q wave asks for K one chunk ahead only: the K wave has brought those rows to the L2.
-    constexpr int KDEPTH = IS_Q ? 1 : DEPTH;
-    Raw<Tin> kr[KDEPTH][2][NM], qr[IS_Q ? DEPTH : 1][2][NM];
-    auto load = [&](int s, int at, bool of_k, bool of_q) {
+// Rows of a tensor [b, :, kh, :] in tile fragments: lane (row, quad) takes eight channels.
+template <typename Tin, int K, bool BACK>
+struct Rows {
+    static constexpr int NP = input_pieces<Tin>(), NM = K / 32;
+    static constexpr int DEPTH = std::is_same<Tin, float>::value ? 1 : 2;  // chunks in flight
+    const Place &w;
+    const Tin *base;
+    size_t stride;
+    unsigned at0;
+    Raw<Tin> raw[DEPTH][2][NM];
+    __device__ __forceinline__ Rows(const void *p, const ChainArgs &a, const Place &w_) : w(w_)
+    {
+        stride = static_cast<size_t>(a.Hk) * K;
+        base = static_cast<const Tin *>(p) + (w.tok0 * a.Hk + w.kh) * K;
+        at0 = static_cast<unsigned>((w.row * stride + 8 * w.quad) * sizeof(Tin));
+    }
+    __device__ __forceinline__ int first(int s) const { return (BACK ? w.n - 1 - s : s) * C; }
+    __device__ __forceinline__ void load(int s, int at)
+    {
         if (s >= w.n)
             return;
-        const int first = chunk(s) * C;
-        const Tin *k = kp + first * stride, *q = qp + first * stride;
-        if (first + C <= w.L) {
+        const int f = first(s);
+        const Tin *p = base + f * stride;
+        if (f + C <= w.L) {
 #pragma unroll
             for (int tau = 0; tau < 2; ++tau)
 #pragma unroll
-                for (int m = 0; m < NM; ++m) {
-                    if (of_k)
-                        kr[IS_Q ? 0 : at][tau][m].load(&lane_at(k + 16 * tau * stride + 32 * m, at0));
-                    if (IS_Q && of_q)
-                        qr[IS_Q ? at : 0][tau][m].load(&lane_at(q + 16 * tau * stride + 32 * m, at0));
-                }
+                for (int m = 0; m < NM; ++m)
+                    raw[at][tau][m].load(&lane_at(p + 16 * tau * stride + 32 * m, at0));
         } else {  // rows behind the end: the last one again, cleared before use
 #pragma unroll
             for (int tau = 0; tau < 2; ++tau) {
-                const size_t t = min(16 * tau + row, w.L - 1 - first) * stride + 8 * quad;
+                const size_t t = min(16 * tau + w.row, w.L - 1 - f) * stride + 8 * w.quad;
 #pragma unroll
-                for (int m = 0; m < NM; ++m) {
-                    if (of_k)
-                        kr[IS_Q ? 0 : at][tau][m].load(k + t + 32 * m);
-                    if (IS_Q && of_q)
-                        qr[IS_Q ? at : 0][tau][m].load(q + t + 32 * m);
-                }
+                for (int m = 0; m < NM; ++m)
+                    raw[at][tau][m].load(p + t + 32 * m);
             }
         }
-    };
-    s16x8 held[2][NM][NP];  // rows that go to LDS in the next iteration
-    u32x2 mat[3][NA];       // and tiles of A
-    // the rows of a tile: their power of two, fp16 fragments to `f`; returns what undoes the power
-    auto convert = [&](const Raw<Tin>(&r)[NM], s16x8(&f)[NM][NP]) {
-        uint32_t top = 0;
+    }
+    __device__ __forceinline__ void clear_behind(int s, int at)
+    {
+        const int f = first(s);
+        if (f + C > w.L)
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
-            top = max(top, r[m].top());
-        const int e = exponent(quad_max(top));
-        const float down = pow2(-e);
+            for (int tau = 0; tau < 2; ++tau)
+                if (f + 16 * tau + w.row >= w.L)
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
-            r[m].planes(down, m1, f[m]);
-        return pow2(e);
-    };
+                    for (int m = 0; m < NM; ++m)
+                        raw[at][tau][m].clear();
+    }
+    // fp16 fragments of the rows with their power of two; fac undoes it.  `self`: the diagonal
+    // tiles of the rows' products with themselves (bf16 inputs).
+    __device__ __forceinline__ void convert(int at, const f32x4 (&self)[2], float m1, s16x8 (&f)[2][NM][NP],
+                                            float (&fac)[2]) const
+    {
+        fac[0] = fac[1] = 1.f;
+        if constexpr (NP == 1) {
+            // |x|^2 of this lane's rows, from the lanes that hold the diagonal
+            bool plain = true;
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau) {
+                const f32x4 &d = self[tau];
+                const float lo = w.row & 1 ? d[1] : d[0], hi = w.row & 1 ? d[3] : d[2];
+                const float sq = __shfl(w.row & 2 ? hi : lo, 16 * (w.row >> 2) + w.row);
+                plain = plain && ((sq >= 0x1p-6f && sq <= 4.f) || sq == 0.f);
+            }
+            if (__all(plain)) {  // rows of norms in [1/8, 2]: fp16 holds them as they are
+#pragma unroll
+                for (int tau = 0; tau < 2; ++tau)
+#pragma unroll
+                    for (int m = 0; m < NM; ++m)
+                        raw[at][tau][m].planes(m1, f[tau][m]);
+                return;
+            }
+        }
+#pragma unroll
+        for (int tau = 0; tau < 2; ++tau) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+                top = max(top, raw[at][tau][m].top());
+            const int e = exponent(quad_max(top));
+            const float down = pow2(-e);
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+                raw[at][tau][m].planes(down, m1, f[tau][m]);
+            fac[tau] = pow2(e);
+        }
+    }
+    // to LDS, [piece][row][channel]
+    __device__ __forceinline__ void put(const s16x8 (&f)[2][NM][NP], uint16_t (*to)[C][K + 16]) const
+    {
+#pragma unroll
+        for (int tau = 0; tau < 2; ++tau)
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+#pragma unroll
+                for (int p = 0; p < NP; ++p)
+                    *reinterpret_cast<s16x8 *>(&to[p][16 * tau + w.row][32 * m + 8 * w.quad]) = f[tau][m][p];
+    }
+};
+
+// The rows of K and X of chunk s + 2.
+template <typename Tin, int K, bool BACK, typename SM>
+__device__ __forceinline__ void k_wave(SM &sm, const ChainArgs &a, const Place &w)
+{
+    constexpr int NP = input_pieces<Tin>(), NM = K / 32;
+    using R = Rows<Tin, K, BACK>;
+    const int row = w.row, quad = w.quad;
+    const float m1 = minus_one();
+    R rows(a.k, a, w);
+    int slot = 0;  // s % 3
     auto body = [&](int it, auto at) {
         const int s = it + 2;
-        if (s >= 1 && s <= w.n) {
-            const int slot = (s - 1) & 1;
+        if (s >= 0 && s < w.n) {
+            rows.clear_behind(s, at);
+            f32x4 acc[3];
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+            s16x8 f[2][NM][NP];
+            float fac[2];
+            if constexpr (NP == 1) {
+#pragma unroll
+                for (int m = 0; m < NM; ++m) {
+                    s16x8 kb[2][1];
+#pragma unroll
+                    for (int tau = 0; tau < 2; ++tau)
+                        rows.raw[at][tau][m].bf16(kb[tau]);
+#pragma unroll
+                    for (int e = 0; e < 3; ++e)
+                        mma<1, 1>(acc[e], kb[e > 0], kb[e > 1]);
+                }
+            }
+            const f32x4 self[2] = {acc[0], acc[2]};
+            rows.convert(at, self, m1, f, fac);
+            rows.load(s + R::DEPTH, at);
+            rows.put(f, sm.k[slot]);
+            slot = slot == 2 ? 0 : slot + 1;
+            if (quad == 0) {
+                sm.kf[row] = fac[0];
+                sm.kf[16 + row] = fac[1];
+            }
+            if constexpr (NP != 1)
+#pragma unroll
+                for (int m = 0; m < NM; ++m)
+#pragma unroll
+                    for (int e = 0; e < 3; ++e)
+                        mmah<NP, NP>(acc[e], f[e > 0][m], f[e > 1][m]);
+            wave_lds_fence();
+            if constexpr (NP != 1)
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                    acc[e] *= fac[e > 1] * *reinterpret_cast<const f32x4 *>(&sm.kf[16 * (e > 0) + 4 * quad]);
+            const float *head = sm.head[s & 3], *tail = sm.tail[s & 3];
+            const float *beta = sm.vec[s & 3][2];
+            if (w.lane < C) {
+                const int l = w.lane;
+                const float kf = sm.kf[l];
+                sm.con[s & 3][0][l] = (BACK ? sm.vec[s & 3][1][l] : sm.vec[s & 3][0][l]) * kf;
+                sm.con[s & 3][1][l] = (BACK ? -sm.vec[s & 3][3][l] : sm.vec[s & 3][1][l]) * kf;
+                sm.bk[s & 3][l] = BACK ? kf : beta[l] * kf;
+            }
+            // lane: column j; registers: rows i
+#pragma unroll
+            for (int e = 0; e < 3; ++e) {
+                const int ti = e > 0, tj = e > 1, i0 = 16 * ti + 4 * quad, j = 16 * tj + row;
+                f32x4 v, x;
+                if constexpr (BACK)
+                    x = *reinterpret_cast<const f32x4 *>(&beta[i0]) * acc[e];
+                else
+                    x = beta[j] * acc[e];
+                if (e == 1) {
+                    v = x * (tail[j] * *reinterpret_cast<const f32x4 *>(&head[i0]));
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float y = sm.p[s & 3][ti][4 * quad + r][row] * x[r];
+                        v[r] = row < 4 * quad + r ? y : 0.f;
+                    }
+                }
+                *reinterpret_cast<f32x4 *>(&sm.x[s & 1][j][i0]) = v;
+            }
+        }
+        __syncthreads();
+    };
+#pragma unroll
+    for (int i = 0; i < R::DEPTH; ++i)
+        rows.load(i, i);
+    // the buffer in use alternates from chunk 0, which iteration -2 takes
+    for (int it = -3;;) {
+        body(it, std::integral_constant<int, R::DEPTH - 1>{});
+        if (++it == w.n)
+            break;
+        body(it, std::integral_constant<int, 0>{});
+        if (++it == w.n)
+            break;
+    }
+}
+
+// The rows of Q and A of chunk s + 1, with the rows of K that the K wave has left in LDS.
+template <typename Tin, int K, int NA, bool BACK, typename SM>
+__device__ __forceinline__ void q_wave(SM &sm, const ChainArgs &a, const Place &w)
+{
+    constexpr int NP = input_pieces<Tin>(), NM = K / 32;
+    using R = Rows<Tin, K, BACK>;
+    const int row = w.row, quad = w.quad;
+    const float m1 = minus_one();
+    R rows(a.q, a, w);
+    int slot = 0;  // s % 3
+    auto body = [&](int it, auto at) {
+        const int s = it + 1;
+        if (s >= 0 && s < w.n) {
+            s16x8 kh[2][NM][NP];
 #pragma unroll
             for (int tau = 0; tau < 2; ++tau)
 #pragma unroll
                 for (int m = 0; m < NM; ++m)
 #pragma unroll
                     for (int p = 0; p < NP; ++p)
-                        *reinterpret_cast<s16x8 *>(IS_Q ? &sm.q[slot][p][16 * tau + row][32 * m + 8 * quad]
-                                                        : &sm.k[slot][p][16 * tau + row][32 * m + 8 * quad]) =
-                            held[tau][m][p];
-            if constexpr (IS_Q)
-#pragma unroll
-                for (int e = 0; e < 3; ++e) {
-                    const int ti = e > 0, tj = e > 1;
-#pragma unroll
-                    for (int p = 0; p < NA; ++p)
-                        *reinterpret_cast<u32x2 *>(
-                            &sm.a[slot][p][16 * (BACK ? tj : ti) + row][8 * quad + 4 * (BACK ? ti : tj)]) = mat[e][p];
-                }
-        }
-        if (s >= 0 && s < w.n) {
-            const int t0 = chunk(s) * C + row;
-            f32x4 acc[3], self[2];  // self: Q Q^T's diagonal tiles (Q wave)
+                        kh[tau][m][p] = lds8(&sm.k[slot][p][16 * tau + row][32 * m + 8 * quad]);
+            slot = slot == 2 ? 0 : slot + 1;
+            rows.clear_behind(s, at);
+            f32x4 acc[3], self[2];
 #pragma unroll
             for (int e = 0; e < 3; ++e)
                 acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
             self[0] = self[1] = acc[0];
-            if (chunk(s) * C + C > w.L)
-#pragma unroll
-                for (int tau = 0; tau < 2; ++tau)
-                    if (t0 + 16 * tau >= w.L)
-#pragma unroll
-                        for (int m = 0; m < NM; ++m) {
-                            kr[IS_Q ? 0 : static_cast<int>(at)][tau][m].clear();
-                            if constexpr (IS_Q)
-                                qr[at][tau][m].clear();
-                        }
-            // lane: column of the tile; registers: rows 4 quad ..  The Q wave's forward tiles
-            // are transposed, as A's rows are stored.
-            float fac[2] = {1.f, 1.f}, kfac[2] = {1.f, 1.f};
-            if constexpr (NP == 1) {
-#pragma unroll
-                for (int m = 0; m < NM; ++m) {
-                    s16x8 kb[2][1], qb[2][1];
-#pragma unroll
-                    for (int tau = 0; tau < 2; ++tau) {
-                        kr[IS_Q ? 0 : static_cast<int>(at)][tau][m].bf16(kb[tau]);
-                        if constexpr (IS_Q)
-                            qr[at][tau][m].bf16(qb[tau]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 3; ++e) {
-                        const int ti = e > 0, tj = e > 1;
-                        if constexpr (!IS_Q)
-                            mma<1, 1>(acc[e], kb[ti], kb[tj]);
-                        else if constexpr (BACK)
-                            mma<1, 1>(acc[e], qb[ti], kb[tj]);
-                        else
-                            mma<1, 1>(acc[e], kb[tj], qb[ti]);
-                    }
-                    if constexpr (IS_Q)
-#pragma unroll
-                        for (int tau = 0; tau < 2; ++tau)
-                            mma<1, 1>(self[tau], qb[tau], qb[tau]);
-                }
-                if constexpr (!IS_Q) {
-                    self[0] = acc[0];
-                    self[1] = acc[2];
-                }
-                if (IS_Q)
-                    load(s + 1, 0, true, false);
-                // |x|^2 of this lane's rows, from the lanes that hold the diagonal
-                bool plain = true;
-#pragma unroll
-                for (int tau = 0; tau < 2; ++tau) {
-                    const f32x4 &d = self[tau];
-                    const float lo = row & 1 ? d[1] : d[0], hi = row & 1 ? d[3] : d[2];
-                    const float sq = __shfl(row & 2 ? hi : lo, 16 * (row >> 2) + row);
-                    plain = plain && ((sq >= 0x1p-6f && sq <= 4.f) || sq == 0.f);
-                }
-                if (__all(plain)) {  // rows of norms in [1/8, 2]: fp16 holds them as they are
-#pragma unroll
-                    for (int tau = 0; tau < 2; ++tau)
-#pragma unroll
-                        for (int m = 0; m < NM; ++m)
-                            if constexpr (IS_Q)
-                                qr[at][tau][m].planes(m1, held[tau][m]);
-                            else
-                                kr[at][tau][m].planes(m1, held[tau][m]);
-                } else {
-#pragma unroll
-                    for (int tau = 0; tau < 2; ++tau)
-                        if constexpr (IS_Q)
-                            fac[tau] = convert(qr[at][tau], held[tau]);
-                        else
-                            fac[tau] = convert(kr[at][tau], held[tau]);
-                }
-            } else {  // fp32: the products run on the fp16 pieces too
-                s16x8 kh[2][NM][NP];
-#pragma unroll
-                for (int tau = 0; tau < 2; ++tau) {
-                    if constexpr (IS_Q) {
-                        kfac[tau] = convert(kr[0][tau], kh[tau]);
-                        fac[tau] = convert(qr[0][tau], held[tau]);
-                    } else {
-                        fac[tau] = kfac[tau] = convert(kr[0][tau], held[tau]);
-                    }
-                }
-                if (IS_Q)
-                    load(s + 1, 0, true, false);
+            s16x8 f[2][NM][NP];
+            float fac[2];
+            if constexpr (NP == 1)
 #pragma unroll
                 for (int m = 0; m < NM; ++m)
 #pragma unroll
-                    for (int e = 0; e < 3; ++e) {
-                        const int ti = e > 0, tj = e > 1;
-                        if constexpr (!IS_Q)
-                            mmah<NP, NP>(acc[e], held[ti][m], held[tj][m]);
-                        else if constexpr (BACK)
-                            mmah<NP, NP>(acc[e], held[ti][m], kh[tj][m]);
-                        else
-                            mmah<NP, NP>(acc[e], kh[tj][m], held[ti][m]);
+                    for (int tau = 0; tau < 2; ++tau) {
+                        s16x8 qb[1];
+                        rows.raw[at][tau][m].bf16(qb);
+                        mma<1, 1>(self[tau], qb, qb);
                     }
-                if (IS_Q && quad == 0)
-#pragma unroll
-                    for (int tau = 0; tau < 2; ++tau)
-                        sm.kq[16 * tau + row] = kfac[tau];
+            rows.convert(at, self, m1, f, fac);
+            rows.load(s + R::DEPTH, at);
+            rows.put(f, sm.q[s & 1]);
+            if (quad == 0) {
+                sm.qf[row] = fac[0];
+                sm.qf[16 + row] = fac[1];
             }
-            if (quad == 0)
+            // forward: lane: row i of A; registers: columns j.  Backward: transposed.
 #pragma unroll
-                for (int tau = 0; tau < 2; ++tau)
-                    (IS_Q ? sm.qf : sm.kf)[16 * tau + row] = fac[tau];
-            load(s + DEPTH, at, !IS_Q, IS_Q);
-            wave_lds_fence();
-            if constexpr (NP != 1)  // the powers of both rows
+            for (int m = 0; m < NM; ++m)
 #pragma unroll
                 for (int e = 0; e < 3; ++e) {
-                    const int ti = e > 0, tj = e > 1;
-                    if constexpr (IS_Q && !BACK)
-                        acc[e] *= fac[ti] * *reinterpret_cast<const f32x4 *>(&sm.kq[16 * tj + 4 * quad]);
+                    if constexpr (BACK)
+                        mmah<NP, NP>(acc[e], f[e > 0][m], kh[e > 1][m]);
                     else
-                        acc[e] *= kfac[tj] * *reinterpret_cast<const f32x4 *>(&(IS_Q ? sm.qf : sm.kf)[16 * ti + 4 * quad]);
+                        mmah<NP, NP>(acc[e], kh[e > 1][m], f[e > 0][m]);
                 }
-            const float *head = sm.head[s & 1], *tail = sm.tail[s & 1];
-            const float *beta = sm.vec[s & 3][2];
-            if (w.lane < C) {
-                const int l = w.lane;
-                if constexpr (IS_Q) {
-                    sm.con[s & 3][2][l] = a.scale * sm.vec[s & 3][0][l] * sm.qf[l];
-                } else {
-                    sm.con[s & 3][0][l] = (BACK ? sm.vec[s & 3][1][l] : sm.vec[s & 3][0][l]) * sm.kf[l];
-                    sm.con[s & 3][1][l] = (BACK ? -sm.vec[s & 3][3][l] : sm.vec[s & 3][1][l]) * sm.kf[l];
-                }
-            }
+            wave_lds_fence();
+            const float *head = sm.head[s & 3], *tail = sm.tail[s & 3], *bk = sm.bk[s & 3];
+            if (w.lane < C)
+                sm.con[s & 3][2][w.lane] = a.scale * sm.vec[s & 3][0][w.lane] * sm.qf[w.lane];
 #pragma unroll
             for (int e = 0; e < 3; ++e) {
                 const int ti = e > 0, tj = e > 1;
                 f32x4 v;
-                if constexpr (IS_Q && !BACK) {
+                if constexpr (!BACK) {
                     const int i = 16 * ti + row, j0 = 16 * tj + 4 * quad;
-                    const f32x4 x = (a.scale * *reinterpret_cast<const f32x4 *>(&beta[j0])) * acc[e];
+                    const f32x4 x = ((a.scale * fac[ti]) * *reinterpret_cast<const f32x4 *>(&bk[j0])) * acc[e];
                     if (e == 1) {
                         v = x * (head[i] * *reinterpret_cast<const f32x4 *>(&tail[j0]));
                     } else {
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            const float y = sm.p[s & 1][ti][row][4 * quad + r] * x[r];
+                            const float y = sm.p[s & 3][ti][row][4 * quad + r] * x[r];
                             v[r] = 4 * quad + r <= row ? y : 0.f;
                         }
                     }
                 } else {
                     const int i0 = 16 * ti + 4 * quad, j = 16 * tj + row;
-                    f32x4 x;
-                    if constexpr (!IS_Q && BACK)
-                        x = *reinterpret_cast<const f32x4 *>(&beta[i0]) * acc[e];
-                    else
-                        x = (IS_Q ? a.scale : beta[j]) * acc[e];
+                    const f32x4 x = ((a.scale * bk[j]) * *reinterpret_cast<const f32x4 *>(&sm.qf[i0])) * acc[e];
                     if (e == 1) {
                         v = x * (tail[j] * *reinterpret_cast<const f32x4 *>(&head[i0]));
                     } else {
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            const float y = sm.p[s & 1][ti][4 * quad + r][row] * x[r];
-                            v[r] = (IS_Q ? row <= 4 * quad + r : row < 4 * quad + r) ? y : 0.f;
+                            const float y = sm.p[s & 3][ti][4 * quad + r][row] * x[r];
+                            v[r] = row <= 4 * quad + r ? y : 0.f;
                         }
                     }
                 }
-                if constexpr (IS_Q)
-                    split4<NA>(v, mat[e]);
-                else
-                    *reinterpret_cast<f32x4 *>(&sm.x[s & 1][16 * tj + row][16 * ti + 4 * quad]) = v;
+                u32x2 out[NA];
+                split4<NA>(v, out);
+#pragma unroll
+                for (int p = 0; p < NA; ++p)
+                    *reinterpret_cast<u32x2 *>(
+                        &sm.a[s & 1][p][16 * (BACK ? tj : ti) + row][8 * quad + 4 * (BACK ? ti : tj)]) = out[p];
             }
         }
         __syncthreads();
     };
 #pragma unroll
-    for (int i = 0; i < DEPTH; ++i)
-        load(i, i, !IS_Q, IS_Q);
-    if (IS_Q)
-        load(0, 0, true, false);
-    // the buffer in use alternates from chunk 0, which iteration -2 takes
+    for (int i = 0; i < R::DEPTH; ++i)
+        rows.load(i, i);
+    // the buffer in use alternates from chunk 0, which iteration -1 takes
     for (int it = -3;;) {
-        body(it, std::integral_constant<int, DEPTH - 1>{});
+        body(it, std::integral_constant<int, 0>{});
         if (++it == w.n)
             break;
-        body(it, std::integral_constant<int, 0>{});
+        body(it, std::integral_constant<int, R::DEPTH - 1>{});
         if (++it == w.n)
             break;
     }
@@ -663,11 +701,11 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
         return;
     }
     if (wave == 5) {
-        rows_wave<Tin, K, NA, BACK, true>(sm, a, w);
+        q_wave<Tin, K, NA, BACK>(sm, a, w);
         return;
     }
     if (wave == 4) {
-        rows_wave<Tin, K, NA, BACK, false>(sm, a, w);
+        k_wave<Tin, K, BACK>(sm, a, w);
         return;
     }
 
@@ -807,8 +845,11 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
         if constexpr (MODE != FWD)
             store(a.rows, c * C, R);
     };
+    int kslot = 0;  // s % 3
     for (int s = 0; s < n; ++s) {
         const int slot = s & 1, c = BACK ? n - 1 - s : s;
+        const auto &kr = sm.k[kslot];
+        kslot = kslot == 2 ? 0 : kslot + 1;
         f32x4 v[2];
 #pragma unroll
         for (int tau = 0; tau < 2; ++tau)
@@ -845,7 +886,7 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
         s16x8 kf[NM][2][NP], qf[NM][2][NP];
 #pragma unroll
         for (int m = 0; m < NM; ++m)
-            rows_of(sm.k[slot], m, kf[m]);
+            rows_of(kr, m, kf[m]);
         __builtin_amdgcn_sched_barrier(0);
         if (MODE == FWD && s > 0)
             store_rows(c - 1);
@@ -913,7 +954,7 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
             if constexpr (NP == 1)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
-                    transposed(sm.k[slot], t, kt[t]);
+                    transposed(kr, t, kt[t]);
             __builtin_amdgcn_sched_barrier(0);
             mma2<3, 3>(R[0], R[1], tf[0], tf[1], zp);
             matrix(sm.a[slot], af);
@@ -928,8 +969,8 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
 #pragma unroll
             for (int t = 0; t < NT; t += 2) {
                 if constexpr (NP != 1) {
-                    transposed(sm.k[slot], t, kt[t]);
-                    transposed(sm.k[slot], t + 1, kt[t + 1]);
+                    transposed(kr, t, kt[t]);
+                    transposed(kr, t + 1, kt[t + 1]);
                 }
                 mmah2<NP, 2>(S[t], S[t + 1], kt[t], kt[t + 1], up2);
             }
@@ -965,8 +1006,8 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
                 transposed(sm.q[slot], t, x[0]);
                 transposed(sm.q[slot], t + 1, x[1]);
                 mmah2<NP, 2>(S[t], S[t + 1], x[0], x[1], yp);
-                transposed(sm.k[slot], t, x[0]);
-                transposed(sm.k[slot], t + 1, x[1]);
+                transposed(kr, t, x[0]);
+                transposed(kr, t + 1, x[1]);
                 mmah2<NP, 2>(S[t], S[t + 1], x[0], x[1], up2);
             }
         }
