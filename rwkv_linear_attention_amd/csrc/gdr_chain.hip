@@ -89,11 +89,43 @@ struct Smem {
     float p[4][2][16][17];           // P inside the halves
 };
 
+// The rows of one chunk as a buffer: offsets from its first element are 32-bit, a load behind
+// the last of `rows` rows gives 0 and a store there does nothing, so the last chunk of a
+// sequence takes no path of its own.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+template <typename T>
+__device__ __forceinline__ Buffer chunk_rows(T *p, int rows, size_t stride)
+{
+    const unsigned bytes = static_cast<unsigned>(min(rows, C)) * static_cast<unsigned>(stride * sizeof(T));
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(static_cast<const void *>(p)), static_cast<short>(0),
+                                             static_cast<int>(bytes), 0x00027000);
+}
+__device__ __forceinline__ void fetch(float &x, Buffer b, unsigned at)
+{
+    x = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, at, 0, 0));
+}
+__device__ __forceinline__ void fetch(uint16_t &x, Buffer b, unsigned at)
+{
+    x = __builtin_amdgcn_raw_buffer_load_b16(b, at, 0, 0);
+}
+// Two fp32 values to two places.
+__device__ __forceinline__ void put2(const float *, Buffer b, unsigned at0, unsigned at1, float x, float y)
+{
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), b, at0, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y), b, at1, 0, 0);
+}
+__device__ __forceinline__ void put2(const uint16_t *, Buffer b, unsigned at0, unsigned at1, float x, float y)
+{
+    const uint32_t u = pk_bf16(x, y);
+    __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(u), b, at0, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(u >> 16), b, at1, 0, 0);
+}
+
 // Eight input elements of a row.
 template <typename Tin> struct Raw;
 template <> struct Raw<uint16_t> {
     u32x4 x;
-    __device__ void load(const uint16_t *p) { x = *reinterpret_cast<const u32x4 *>(p); }
+    __device__ void load(Buffer b, unsigned at) { x = __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, 0); }
     // the largest magnitude, as fp32 bits
     __device__ uint32_t top() const
     {
@@ -115,14 +147,13 @@ template <> struct Raw<uint16_t> {
                    f32x4{bf16_lo(x[2]) * f, bf16_hi(x[2]) * f, bf16_lo(x[3]) * f, bf16_hi(x[3]) * f}, out, m1);
     }
     __device__ void bf16(s16x8 (&out)[1]) const { out[0] = __builtin_bit_cast(s16x8, x); }
-    __device__ void clear() { x = u32x4{0, 0, 0, 0}; }
 };
 template <> struct Raw<float> {
     f32x4 x, y;
-    __device__ void load(const float *p)
+    __device__ void load(Buffer b, unsigned at)
     {
-        x = *reinterpret_cast<const f32x4 *>(p);
-        y = *reinterpret_cast<const f32x4 *>(p + 4);
+        x = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, 0));
+        y = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, at + 16, 0, 0));
     }
     __device__ uint32_t top() const
     {
@@ -133,7 +164,6 @@ template <> struct Raw<float> {
         return m;
     }
     __device__ void planes(float f, float m1, s16x8 (&out)[2]) const { split8h<2>(x * f, y * f, out, m1); }
-    __device__ void clear() { x = y = f32x4{0.f, 0.f, 0.f, 0.f}; }
 };
 
 // The exponent e of a row or column whose largest magnitude has these fp32 bits: 2^-e brings
@@ -144,31 +174,6 @@ __device__ __forceinline__ int exponent(uint32_t bits)
     return bits == 0 || e == 255 ? 0 : min(max(e - 126, -120), 120);
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
-
-// The element `bytes` behind a base that is the same for the whole wave: one 32-bit offset a lane.
-template <typename T>
-__device__ __forceinline__ T &lane_at(T *p, unsigned bytes)
-{
-    return *reinterpret_cast<T *>(reinterpret_cast<char *>(p) + bytes);
-}
-template <typename T>
-__device__ __forceinline__ const T &lane_at(const T *p, unsigned bytes)
-{
-    return *reinterpret_cast<const T *>(reinterpret_cast<const char *>(p) + bytes);
-}
-
-// Two elements, each to an address of its own.
-__device__ __forceinline__ void put2(float &a, float &b, float x, float y)
-{
-    a = x;
-    b = y;
-}
-__device__ __forceinline__ void put2(uint16_t &a, uint16_t &b, float x, float y)
-{
-    const uint32_t u = pk_bf16(x, y);
-    a = static_cast<uint16_t>(u);
-    b = static_cast<uint16_t>(u >> 16);
-}
 
 // What every wave of a workgroup knows.
 struct Place {
@@ -359,7 +364,7 @@ struct Rows {
     const Place &w;
     const Tin *base;
     size_t stride;
-    unsigned at0;
+    unsigned at0;  // this lane's place in the first tile, bytes
     Raw<Tin> raw[DEPTH][2][NM];
     __device__ __forceinline__ Rows(const void *p, const ChainArgs &a, const Place &w_) : w(w_)
     {
@@ -373,33 +378,12 @@ struct Rows {
         if (s >= w.n)
             return;
         const int f = first(s);
-        const Tin *p = base + f * stride;
-        if (f + C <= w.L) {
+        const Buffer b = chunk_rows(base + f * stride, w.L - f, stride);
 #pragma unroll
-            for (int tau = 0; tau < 2; ++tau)
+        for (int tau = 0; tau < 2; ++tau)
 #pragma unroll
-                for (int m = 0; m < NM; ++m)
-                    raw[at][tau][m].load(&lane_at(p + 16 * tau * stride + 32 * m, at0));
-        } else {  // rows behind the end: the last one again, cleared before use
-#pragma unroll
-            for (int tau = 0; tau < 2; ++tau) {
-                const size_t t = min(16 * tau + w.row, w.L - 1 - f) * stride + 8 * w.quad;
-#pragma unroll
-                for (int m = 0; m < NM; ++m)
-                    raw[at][tau][m].load(p + t + 32 * m);
-            }
-        }
-    }
-    __device__ __forceinline__ void clear_behind(int s, int at)
-    {
-        const int f = first(s);
-        if (f + C > w.L)
-#pragma unroll
-            for (int tau = 0; tau < 2; ++tau)
-                if (f + 16 * tau + w.row >= w.L)
-#pragma unroll
-                    for (int m = 0; m < NM; ++m)
-                        raw[at][tau][m].clear();
+            for (int m = 0; m < NM; ++m)
+                raw[at][tau][m].load(b, at0 + static_cast<unsigned>((16 * tau * stride + 32 * m) * sizeof(Tin)));
     }
     // fp16 fragments of the rows with their power of two; fac undoes it.  `self`: the diagonal
     // tiles of the rows' products with themselves (bf16 inputs).
@@ -466,7 +450,6 @@ __device__ __forceinline__ void k_wave(SM &sm, const ChainArgs &a, const Place &
     auto body = [&](int it, auto at) {
         const int s = it + 2;
         if (s >= 0 && s < w.n) {
-            rows.clear_behind(s, at);
             f32x4 acc[3];
 #pragma unroll
             for (int e = 0; e < 3; ++e)
@@ -573,7 +556,6 @@ __device__ __forceinline__ void q_wave(SM &sm, const ChainArgs &a, const Place &
                     for (int p = 0; p < NP; ++p)
                         kh[tau][m][p] = lds8(&sm.k[slot][p][16 * tau + row][32 * m + 8 * quad]);
             slot = slot == 2 ? 0 : slot + 1;
-            rows.clear_behind(s, at);
             f32x4 acc[3], self[2];
 #pragma unroll
             for (int e = 0; e < 3; ++e)
@@ -716,10 +698,12 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
     const size_t vs = static_cast<size_t>(a.H) * a.V;
     // [b, 0, h, 0] of v, o, resid, d_o, and this lane's place in the rows of a chunk
     const size_t row0 = (w.tok0 * a.H + w.h) * a.V;
-    unsigned at[4];  // elements; bytes once multiplied by their size
+    unsigned at[2][4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-        at[r] = static_cast<unsigned>((4 * quad + r) * vs + col);
+    for (int tau = 0; tau < 2; ++tau)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            at[tau][r] = static_cast<unsigned>((16 * tau + 4 * quad + r) * vs + col);
     const size_t st0 = static_cast<size_t>(head) * K * a.V + col;  // [b, h, 0, col] of a state
     auto channel = [&](int t, int r) { return 32 * (t >> 1) + 8 * quad + 4 * (t & 1) + r; };
     using Trow = typename std::conditional<BACK, float, Tin>::type;
@@ -793,42 +777,22 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
     Trow next[2][4];
     auto load = [&](int s) {
         const int first = (BACK ? n - 1 - s : s) * C;
-        const Trow *p = in + first * vs;
-        if (first + C <= L) {
+        const Buffer b = chunk_rows(in + first * vs, L - first, vs);
 #pragma unroll
-            for (int tau = 0; tau < 2; ++tau)
+        for (int tau = 0; tau < 2; ++tau)
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    next[tau][r] = lane_at(p + 16 * tau * vs, at[r] * static_cast<unsigned>(sizeof(Trow)));
-        } else {
-#pragma unroll
-            for (int tau = 0; tau < 2; ++tau)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    next[tau][r] = first + 16 * tau + 4 * quad + r < L
-                                       ? lane_at(p + 16 * tau * vs, at[r] * static_cast<unsigned>(sizeof(Trow)))
-                                       : Trow{0};
-        }
+            for (int r = 0; r < 4; ++r)
+                fetch(next[tau][r], b, at[tau][r] * static_cast<unsigned>(sizeof(Trow)));
     };
     // rows of a chunk, to out[t][col]
     auto store = [&](auto *out, int first, const f32x4(&x)[2]) {
-        auto *p = out + row0 + first * vs;
+        const Buffer b = chunk_rows(out + row0 + first * vs, L - first, vs);
         constexpr unsigned size = sizeof(*out);
-        if (first + C <= L) {
 #pragma unroll
-            for (int tau = 0; tau < 2; ++tau)
+        for (int tau = 0; tau < 2; ++tau)
 #pragma unroll
-                for (int r = 0; r < 4; r += 2)
-                    put2(lane_at(p + 16 * tau * vs, at[r] * size), lane_at(p + 16 * tau * vs, at[r + 1] * size), x[tau][r],
-                         x[tau][r + 1]);
-        } else {
-#pragma unroll
-            for (int tau = 0; tau < 2; ++tau)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (first + 16 * tau + 4 * quad + r < L)
-                        store_elem(&lane_at(p + 16 * tau * vs, at[r] * size), 0, x[tau][r]);
-        }
+            for (int r = 0; r < 4; r += 2)
+                put2(out, b, at[tau][r] * size, at[tau][r + 1] * size, x[tau][r], x[tau][r + 1]);
     };
     if (n > 0)
         load(0);
