@@ -16,8 +16,9 @@
 // products of alphas (a column of P per lane), so no exponent range limits them and
 // alpha = 0 is exact.
 //
-// MAPPING.  A workgroup takes 64 value columns of one head and walks its chunks in order,
-// with one barrier per chunk.  Four consumer waves keep 16 columns of the state each, in
+// MAPPING.  A workgroup takes 64 value columns of one head (fewer where there are few heads)
+// and walks its chunks in order, with one barrier per chunk.  Four (two, one) consumer waves
+// keep 16 columns of the state each, in
 // the accumulator layout of the matrix cores, and do the products above; four producer
 // waves prepare what does not depend on the state, up to three chunks ahead:
 //     decay wave  (s + 3)  P, gamma and the vectors derived from them
@@ -48,7 +49,6 @@ namespace gdr {
 namespace {
 
 constexpr int C = 32;          // tokens of a chunk
-constexpr int COLS = 64;       // value columns of a workgroup
 constexpr int LDT = C + 8;     // pitch (bf16) of the 32 x 32 matrices: 16-byte reads without conflicts
 
 enum Mode { FWD, CKPT, BWD };
@@ -655,7 +655,8 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
     __shared__ Smem<K, NP, NA> sm;
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const unsigned item = xcd_item(blockIdx.x, gridDim.x), nblk = a.V / COLS;
+    const int consumers = (blockDim.x >> 6) - 4, cols = 16 * consumers;
+    const unsigned item = xcd_item(blockIdx.x, gridDim.x), nblk = a.V / cols;
     const unsigned head = item / nblk;
     Place w;
     w.lane = threadIdx.x & 63;
@@ -668,33 +669,31 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
     w.n = (w.L + C - 1) / C;
     w.tok0 = static_cast<size_t>(w.b) * a.T;
 
-    for (unsigned i = threadIdx.x; i < sizeof(sm.t) / 4; i += 512)
+    for (unsigned i = threadIdx.x; i < sizeof(sm.t) / 4; i += blockDim.x)
         reinterpret_cast<uint32_t *>(sm.t)[i] = 0;  // the blocks above the diagonal stay 0
-    for (unsigned i = threadIdx.x; i < sizeof(sm.a) / 4; i += 512)
+    for (unsigned i = threadIdx.x; i < sizeof(sm.a) / 4; i += blockDim.x)
         reinterpret_cast<uint32_t *>(sm.a)[i] = 0;
     __syncthreads();
 
-    if (wave == 7) {
-        decay_wave<BACK>(sm, a, w);
-        return;
-    }
-    if (wave == 6) {
-        inverse_wave<BACK>(sm, w);
-        return;
-    }
-    if (wave == 5) {
-        q_wave<Tin, K, NA, BACK>(sm, a, w);
-        return;
-    }
-    if (wave == 4) {
-        k_wave<Tin, K, BACK>(sm, a, w);
+    if (wave >= consumers) {
+        // Wave i runs on SIMD i % 4: with two consumers the heavier two producers get the SIMDs
+        // that these leave free.
+        const int role = (wave - consumers) ^ (consumers == 2 ? 2 : 0);
+        if (role == 0)
+            k_wave<Tin, K, BACK>(sm, a, w);
+        else if (role == 1)
+            consumers == 2 ? decay_wave<BACK>(sm, a, w) : q_wave<Tin, K, NA, BACK>(sm, a, w);
+        else if (role == 2)
+            inverse_wave<BACK>(sm, w);
+        else
+            consumers == 2 ? q_wave<Tin, K, NA, BACK>(sm, a, w) : decay_wave<BACK>(sm, a, w);
         return;
     }
 
     // -------------------------------------------------------------------- consumers
     const int lane = w.lane, row = w.row, quad = w.quad, n = w.n, L = w.L;
     const float m1 = minus_one();
-    const int col = (item % nblk) * COLS + 16 * wave + row;
+    const int col = (item % nblk) * cols + 16 * wave + row;
     const size_t vs = static_cast<size_t>(a.H) * a.V;
     // [b, 0, h, 0] of v, o, resid, d_o, and this lane's place in the rows of a chunk
     const size_t row0 = (w.tok0 * a.H + w.h) * a.V;
@@ -992,7 +991,14 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
 template <typename Tin, typename Tout, int MODE>
 hipError_t launch_k(const ChainArgs &a, int K, hipStream_t stream)
 {
-    const dim3 grid(static_cast<unsigned>(static_cast<long long>(a.B) * a.H * (a.V / COLS))), block(512);
+    // Consumer waves of a workgroup: four (64 columns), or two or one while that many more
+    // workgroups still fit the 256 compute units side by side.  A consumer with its SIMD to
+    // itself walks faster (2048 tokens, 64 x 64 heads: 32 heads 96 us with four, 79 with two, 71
+    // with one; 96 heads 96, 85 and, in two rounds, 145; 128 wide columns of 128 channels 126,
+    // 113 and 194), at the price of preparing the same chunk in each workgroup.
+    const long long units = static_cast<long long>(a.B) * a.H * (a.V / 64);
+    const int consumers = units * 4 <= 256 ? 1 : units * 2 <= 256 ? 2 : 4;
+    const dim3 grid(static_cast<unsigned>(units * (4 / consumers))), block(64 * (4 + consumers));
     if (K == 64)
         hipLaunchKernelGGL((gdr_chain_kernel<Tin, Tout, 64, MODE>), grid, block, 0, stream, a);
     else

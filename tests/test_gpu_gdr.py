@@ -57,6 +57,17 @@ def test_against_the_oracle(lib, entry, B, T, Hk, H, K, V, dtype, out):
     check(s, ref_s, TOL, "state", HEADS_STATE)
 
 
+@pytest.mark.parametrize("B,H,V", [(1, 2, 64), (5, 13, 64), (3, 22, 128), (9, 15, 64)])
+def test_every_width_of_a_workgroup(lib, B, H, V):
+    """Few heads split into narrower workgroups (1, 2 or 4 waves of 16 columns): rows of each."""
+    inp = make(B, 41, 1, H, 64, V, seed=B)
+    ref_o, ref_s, _ = gdr.forward(*(inp[n] for n in NAMES), inp["state"], 0.125)
+    d = on_gpu(inp)
+    o, s = lib.gdr_forward(*(d[n] for n in NAMES), d["state"])
+    check_o(o, ref_o, "o")
+    check(s, ref_s, TOL, "state", HEADS_STATE)
+
+
 @pytest.mark.parametrize("T", [3, 40])
 @pytest.mark.parametrize("entry", ["forward", "step"])
 def test_without_a_state_in_place_and_with_a_scale(lib, entry, T):
