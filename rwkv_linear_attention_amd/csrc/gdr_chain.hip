@@ -646,6 +646,31 @@ __device__ __forceinline__ void q_wave(SM &sm, const ChainArgs &a, const Place &
     }
 }
 
+// Workgroup index to (row, head, columns): the workgroups that read the same query / key head
+// (`share` of them, next to each other) go to one XCD and its L2, the next such group to the
+// next XCD.  (Consecutive workgroups go round the 8 XCDs.)
+__device__ __forceinline__ unsigned chain_item(unsigned bid, unsigned n, unsigned share)
+{
+    const unsigned rounds = n / (8 * share) * 8 * share;
+    if (bid >= rounds)
+        return bid;
+    const unsigned x = bid & 7, i = bid >> 3;
+    return (i / share * 8 + x) * share + i % share;
+}
+
+// The row of rank r by length, the longest first: workgroups start in this order, so the long
+// rows do not wait for a compute unit while short ones hold them.
+__device__ __forceinline__ int by_length(const int *lengths, int B, int T, int r, int lane)
+{
+    const int own = lane < B ? min(max(lengths[lane], 0), T) : -1;
+    int rank = 0;
+    for (int i = 0; i < B; ++i) {
+        const int x = __builtin_amdgcn_readlane(own, i);
+        rank += x > own || (x == own && i < lane);
+    }
+    return __builtin_amdgcn_readfirstlane(__ffsll(__ballot(lane < B && rank == r)) - 1);
+}
+
 template <typename Tin, typename Tout, int K, int MODE>
 __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
 {
@@ -656,14 +681,17 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int consumers = (blockDim.x >> 6) - 4, cols = 16 * consumers;
-    const unsigned item = xcd_item(blockIdx.x, gridDim.x), nblk = a.V / cols;
-    const unsigned head = item / nblk;
+    const unsigned nblk = a.V / cols;
+    const unsigned item = chain_item(blockIdx.x, gridDim.x, nblk * (a.H / a.Hk));
     Place w;
     w.lane = threadIdx.x & 63;
     w.row = w.lane & 15;
     w.quad = w.lane >> 4;
-    w.b = head / a.H;
-    w.h = head % a.H;
+    w.b = item / nblk / a.H;
+    w.h = item / nblk % a.H;
+    if (a.lengths && a.B <= 64)
+        w.b = by_length(a.lengths, a.B, a.T, w.b, w.lane);
+    const unsigned head = w.b * a.H + w.h;
     w.kh = w.h / (a.H / a.Hk);
     w.L = a.lengths ? min(max(a.lengths[w.b], 0), a.T) : a.T;
     w.n = (w.L + C - 1) / C;

@@ -108,6 +108,20 @@ def test_lengths(lib, T, lengths):
     check(s, ref_s, TOL, "state", HEADS_STATE)
 
 
+@pytest.mark.parametrize("B", [11, 64, 70])
+def test_many_rows_of_their_own_lengths(lib, B):
+    """Rows start by length (up to 64 of them): each must still be its own."""
+    lengths = torch.randint(0, 60, (B,), generator=torch.Generator().manual_seed(B))
+    lengths[:3] = 17     # ties
+    inp = make(B, 57, 1, 2, 64, 64, seed=B)
+    ref_o, ref_s, _ = gdr.forward(*(inp[n] for n in NAMES), inp["state"], 0.125, lengths.tolist())
+    d = on_gpu(inp)
+    o, s = lib.gdr_forward(*(d[n] for n in NAMES), d["state"], o=torch.zeros(B, 57, 2, 64, device="cuda"),
+                           lengths=lengths)
+    check_o(o, ref_o, "o")
+    check(s, ref_s, TOL, "state", HEADS_STATE)
+
+
 @pytest.mark.parametrize("K,V", [(64, 64), (128, 128)])
 def test_verify_commit_chain(lib, K, V):
     """Serving as it is used: prefill, a verify step over drafts, the drafts judged, the states committed, on."""
