@@ -100,48 +100,52 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
     constexpr int UNITS = VB * K / 4 / 256;  // 16-byte units of a staged state, per thread
     __shared__ Smem<K, NB> sm;
 
-    const int tid = threadIdx.x, lane = tid & 63, row = lane & 15, quad = lane >> 4;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const unsigned item = xcd_item(blockIdx.x, gridDim.x);
     const int kh = item % p.Hk, blk = (item / p.Hk) % nblk, b = item / p.Hk / nblk;
     const int group = p.H / p.Hk, t0 = blk * TB, live = min(p.T - t0, TB);  // tokens of this block
     const size_t tok0 = static_cast<size_t>(b) * p.T + t0;
     const size_t qk0 = (tok0 * p.Hk + kh) * K, qs = static_cast<size_t>(p.Hk) * K;
-    const int mine = 16 * w + row;  // this lane's token as a fragment row
-    const bool on = mine < live;
-
-    // The rows of K or Q to LDS, in bf16 pieces; rows behind the end are 0.
-    auto stage_rows = [&](const void *src) {
-        const Tin *x = static_cast<const Tin *>(src) + qk0;
-        constexpr int N = TB * (K / 8) / 256, STEP = N < 4 ? N : 4;
-#pragma unroll
-        for (int i0 = 0; i0 < N; i0 += STEP) {
-            s16x8 f[STEP][NB];
-#pragma unroll
-            for (int i = 0; i < STEP; ++i) {
-                const int u = tid + 256 * (i0 + i), t = u / (K / 8), c = 8 * (u % (K / 8));
-                fragment(x + min(t, live - 1) * qs + c, f[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < STEP; ++i) {
-                const int u = tid + 256 * (i0 + i), t = u / (K / 8), c = 8 * (u % (K / 8));
-#pragma unroll
-                for (int y = 0; y < NB; ++y)
-                    *reinterpret_cast<s16x8 *>(&sm.rows[y][t][c]) = t < live ? f[i][y] : s16x8{0, 0, 0, 0, 0, 0, 0, 0};
-            }
-        }
-    };
-    // element 16 t + row of staged row 16 w + 4 quad + r
-    auto element = [&](int t, int r) {
-        float y = 0.f;
-#pragma unroll
-        for (int i = NB - 1; i >= 0; --i)
-            y += load_elem(&sm.rows[i][16 * w + 4 * quad + r][16 * t + row], 0);
-        return y;
-    };
-
     for (int hh = 0; hh < group; ++hh) {
         const int h = kh * group + hh;
+        // Addresses are formed per head: hoisted out of this loop, a few hundred of them, they
+        // would spill.
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        const int lane = tid & 63, row = lane & 15, quad = lane >> 4;
+        const int mine = 16 * w + row;  // this lane's token as a fragment row
+        const bool on = mine < live;
+
+        // The rows of K or Q to LDS, in bf16 pieces; rows behind the end are 0.
+        auto stage_rows = [&](const void *src) {
+            const Tin *x = static_cast<const Tin *>(src) + qk0;
+            constexpr int N = TB * (K / 8) / 256, STEP = N < 4 ? N : 4;
+#pragma unroll
+            for (int i0 = 0; i0 < N; i0 += STEP) {
+                s16x8 f[STEP][NB];
+#pragma unroll
+                for (int i = 0; i < STEP; ++i) {
+                    const int u = tid + 256 * (i0 + i), t = u / (K / 8), c = 8 * (u % (K / 8));
+                    fragment(x + min(t, live - 1) * qs + c, f[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < STEP; ++i) {
+                    const int u = tid + 256 * (i0 + i), t = u / (K / 8), c = 8 * (u % (K / 8));
+#pragma unroll
+                    for (int y = 0; y < NB; ++y)
+                        *reinterpret_cast<s16x8 *>(&sm.rows[y][t][c]) = t < live ? f[i][y] : s16x8{0, 0, 0, 0, 0, 0, 0, 0};
+                }
+            }
+        };
+        // element 16 t + row of staged row 16 w + 4 quad + r
+        auto element = [&](int t, int r) {
+            float y = 0.f;
+#pragma unroll
+            for (int i = NB - 1; i >= 0; --i)
+                y += load_elem(&sm.rows[i][16 * w + 4 * quad + r][16 * t + row], 0);
+            return y;
+        };
+
         if (w == 0) {  // decays
             float g = 0.f, beta = 0.f;
             if (lane < live) {
