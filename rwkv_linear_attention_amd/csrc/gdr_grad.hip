@@ -112,9 +112,9 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
         // would spill.
         int tid = threadIdx.x;
         asm volatile("" : "+v"(tid));
-        const int lane = tid & 63, row = lane & 15, quad = lane >> 4;
-        const int mine = 16 * w + row;  // this lane's token as a fragment row
-        const bool on = mine < live;
+        int lane = tid & 63, row = lane & 15, quad = lane >> 4;
+        int mine = 16 * w + row;  // this lane's token as a fragment row
+        bool on = mine < live;
 
         // The rows of K or Q to LDS, in bf16 pieces; rows behind the end are 0.
         auto stage_rows = [&](const void *src) {
@@ -271,6 +271,13 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
         }
 
         db = quad_sum(db);
+        tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));  // as above: nothing of this phase is formed before the columns' loop
+        lane = tid & 63;
+        row = lane & 15;
+        quad = lane >> 4;
+        mine = 16 * w + row;
+        on = mine < live;
         if (quad == 0 && on)
             p.dbeta[(tok0 + mine) * p.H + h] = db;
         // decays on E1, E2 (lane: i = mine; registers: j = 16 t + 4 quad + r), to LDS
