@@ -137,12 +137,16 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
                 }
             }
         };
-        // element 16 t + row of staged row 16 w + 4 quad + r
-        auto element = [&](int t, int r) {
-            float y = 0.f;
+        // staged rows 16 w + 4 quad + r (r = 0..3), channel 16 t + row
+        auto staged = [&](int t) {
+            f32x4 y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = NB - 1; i >= 0; --i)
-                y += load_elem(&sm.rows[i][16 * w + 4 * quad + r][16 * t + row], 0);
+            for (int i = NB - 1; i >= 0; --i) {
+                const s16x4 x = tr4(&sm.rows[i][16 * w + 4 * quad + (row >> 2)][16 * t + 4 * (lane & 3)]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    y[r] += bf16_lo(static_cast<uint16_t>(x[r]));
+            }
             return y;
         };
 
@@ -201,13 +205,14 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
                 g4[i] = *reinterpret_cast<const f32x4 *>(gp + static_cast<size_t>(v) * K + 1024 * i);
             }
             s16x8 fo[3], fv[3], fu[3];
+            if (live < TB)
 #pragma unroll
-            for (int x = 0; x < 3; ++x)
+                for (int x = 0; x < 3; ++x)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
+                    for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        x4[x][e][r] = on ? x4[x][e][r] : 0.f;
+                        for (int r = 0; r < 4; ++r)
+                            x4[x][e][r] = on ? x4[x][e][r] : 0.f;
             split8<3>(x4[0][0], x4[0][1], fo);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -353,25 +358,18 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
             }
         };
         // e and f, while dq, dr and dc hold the states' parts only
-        f32x4 ei, fj;
-        const Tin *q = static_cast<const Tin *>(p.q) + qk0 + row;
+        f32x4 ei = {0.f, 0.f, 0.f, 0.f}, fj = ei;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const Tin *qr = q + static_cast<size_t>(min(16 * w + 4 * quad + r, live - 1)) * qs;
-            float s = 0.f, u = 0.f;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const float k = element(t, r);
-                s = fmaf(load_elem(qr, 16 * t), dq[t][r], fmaf(k, dr[t][r], s));
-                u = fmaf(k, dc[t][r], u);
-            }
-            ei[r] = wkv7::group16_sum(s);
-            fj[r] = wkv7::group16_sum(u);
+        for (int t = 0; t < NT; ++t) {
+            const f32x4 k = staged(t);
+            ei += k * dr[t];
+            fj += k * dc[t];
         }
-        if (row == 0) {
-            *reinterpret_cast<f32x4 *>(&sm.e[16 * w + 4 * quad]) = ei;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            fj[r] = wkv7::group16_sum(fj[r]);
+        if (row == 0)
             *reinterpret_cast<f32x4 *>(&sm.f[16 * w + 4 * quad]) = fj;
-        }
         const float state = wkv7::wave_sum(gs) * sm.gamma[TB - 1];
         if (lane == 0)
             sm.sums[w] = state;
@@ -409,14 +407,14 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
                         if (r)
                             run[r] += run[r - 1];
                     }
-                    // the quads before this one, of the same row
-                    const float own = run[3];
-#pragma unroll
-                    for (int y = 0; y < 3; ++y) {
-                        const float other = __shfl(own, 16 * y + row);
-                        sum += y < quad ? other : 0.f;
-                    }
-                    before += quad_sum(own);
+                    // the quads before this one, of the same row, and all four
+                    const uint32_t own = __float_as_uint(run[3]);
+                    const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(own, own, false, false));
+                    const float pair = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+                    const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(
+                                                                  __float_as_uint(pair), __float_as_uint(pair), false, false));
+                    sum += (quad >= 2 ? __uint_as_float(b[0]) : 0.f) + (quad & 1 ? __uint_as_float(a[0]) : 0.f);
+                    before += __uint_as_float(b[0]) + __uint_as_float(b[1]);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const bool past = t < w || 4 * quad + r < row;  // i >= j + 1
@@ -428,11 +426,27 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
                 }
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t) {
             dr[t] += dc[t];  // dk
-        apply(0, false, dq);
+            dc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        apply(0, false, dc);  // dq's other part, apart until dq has been used
         apply(1, false, dr);
         apply(1, true, dr);
+        __syncthreads();
+        stage_rows(p.q);
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            ei += staged(t) * dq[t];
+            dq[t] += dc[t];
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            ei[r] = wkv7::group16_sum(ei[r]);
+        if (row == 0)
+            *reinterpret_cast<f32x4 *>(&sm.e[16 * w + 4 * quad]) = ei;
+        apply(0, true, dr);
         __syncthreads();
         if (w == 0) {
             float x = sm.e[lane], y = sm.f[lane], z = 0.f;
@@ -450,9 +464,6 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
             if (lane < live)
                 p.dg[(tok0 + lane) * p.H + h] = x;
         }
-        stage_rows(p.q);
-        __syncthreads();
-        apply(0, true, dr);
         // dq, dk: the first head of a group writes, the others add
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
