@@ -52,12 +52,12 @@
 extern "C" {
 #endif
 
-/* Limits (WKV7_ERR_SHAPE beyond them): V <= GDR_MAX_V; T <= GDR_MAX_T; H * V <= GDR_MAX_ROW (a chunk's
- * rows are addressed with 32-bit offsets from its first); B * H * V <= GDR_MAX_COLUMNS and
+/* Limits (WKV7_ERR_SHAPE beyond them): V <= GDR_MAX_V; T <= GDR_MAX_T; H * K and H * V <= GDR_MAX_ROW (the rows
+ * of 64 tokens are addressed with 32-bit offsets from the first); B * H * V <= GDR_MAX_COLUMNS and
  * B * ceil(T/64) * H <= GDR_MAX_BLOCKS (a launch holds fewer than 2^32 threads; the latter
  * for the training pair).  Tensor offsets are 64-bit. */
 #define GDR_MAX_V 512
-#define GDR_MAX_ROW 16777216
+#define GDR_MAX_ROW 8388608
 #define GDR_MAX_T 1073741824
 #define GDR_MAX_BLOCKS 8000000
 #define GDR_MAX_COLUMNS 268435456

@@ -63,7 +63,7 @@ int check_shape(int B, int T, int Hk, int H, int K, int V)
     if (B < 1 || T < 0 || Hk < 1 || H < 1 || H % Hk != 0 || V > GDR_MAX_V)
         return WKV7_ERR_SHAPE;
     const int64_t heads = static_cast<int64_t>(B) * H;
-    if (T > GDR_MAX_T || H > GDR_MAX_ROW / V || heads > GDR_MAX_COLUMNS / V)
+    if (T > GDR_MAX_T || H > GDR_MAX_ROW / (K > V ? K : V) || heads > GDR_MAX_COLUMNS / V)
         return WKV7_ERR_SHAPE;
     // B T H K V 4 bytes (the per-position states, the largest buffer) within int64
     if (T > 0 && heads > INT64_MAX / (static_cast<int64_t>(K) * V * 8) / T)

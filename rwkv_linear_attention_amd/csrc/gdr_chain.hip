@@ -89,17 +89,7 @@ struct Smem {
     float p[4][2][16][17];           // P inside the halves
 };
 
-// The rows of one chunk as a buffer: offsets from its first element are 32-bit, a load behind
-// the last of `rows` rows gives 0 and a store there does nothing, so the last chunk of a
-// sequence takes no path of its own.
-typedef __amdgpu_buffer_rsrc_t Buffer;
-template <typename T>
-__device__ __forceinline__ Buffer chunk_rows(T *p, int rows, size_t stride)
-{
-    const unsigned bytes = static_cast<unsigned>(min(rows, C)) * static_cast<unsigned>(stride * sizeof(T));
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(static_cast<const void *>(p)), static_cast<short>(0),
-                                             static_cast<int>(bytes), 0x00027000);
-}
+// One element, widened or as it is.
 __device__ __forceinline__ void fetch(float &x, Buffer b, unsigned at)
 {
     x = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, at, 0, 0));
@@ -378,7 +368,7 @@ struct Rows {
         if (s >= w.n)
             return;
         const int f = first(s);
-        const Buffer b = chunk_rows(base + f * stride, w.L - f, stride);
+        const Buffer b = rows_buffer(base + f * stride, min(w.L - f, C), stride);
 #pragma unroll
         for (int tau = 0; tau < 2; ++tau)
 #pragma unroll
@@ -804,7 +794,7 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
     Trow next[2][4];
     auto load = [&](int s) {
         const int first = (BACK ? n - 1 - s : s) * C;
-        const Buffer b = chunk_rows(in + first * vs, L - first, vs);
+        const Buffer b = rows_buffer(in + first * vs, min(L - first, C), vs);
 #pragma unroll
         for (int tau = 0; tau < 2; ++tau)
 #pragma unroll
@@ -813,7 +803,7 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
     };
     // rows of a chunk, to out[t][col]
     auto store = [&](auto *out, int first, const f32x4(&x)[2]) {
-        const Buffer b = chunk_rows(out + row0 + first * vs, L - first, vs);
+        const Buffer b = rows_buffer(out + row0 + first * vs, min(L - first, C), vs);
         constexpr unsigned size = sizeof(*out);
 #pragma unroll
         for (int tau = 0; tau < 2; ++tau)

@@ -70,6 +70,19 @@ __device__ __forceinline__ void store4(uint16_t *p, const f32x4 x)
     *reinterpret_cast<u32x2 *>(p) = u32x2{lo, hi};
 }
 
+// `rows` rows of a tensor as a buffer: offsets from the first element are 32-bit, a load behind
+// the last row gives 0 and a store there does nothing, so the last rows of a sequence take no
+// path of their own.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+template <typename T>
+__device__ __forceinline__ Buffer rows_buffer(T *p, int rows, size_t stride)
+{
+    const unsigned bytes = static_cast<unsigned>(rows) * static_cast<unsigned>(stride * sizeof(T));
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(static_cast<const void *>(p)), static_cast<short>(0),
+                                             static_cast<int>(bytes), 0x00027000);
+}
+__device__ __forceinline__ u32x4 fetch4(Buffer b, unsigned at) { return __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, 0); }
+
 // Workgroup index to work item: consecutive workgroups go round the 8 XCDs, so each XCD
 // gets one contiguous run of items, and items that share inputs meet in its L2.
 __device__ __forceinline__ unsigned xcd_item(unsigned bid, unsigned n)

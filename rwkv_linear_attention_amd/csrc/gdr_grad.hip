@@ -84,10 +84,13 @@ __device__ __forceinline__ void walk(float alpha, int row, float &p, float &all,
 }
 
 // Eight elements of a row as bf16 pieces.
-__device__ __forceinline__ void fragment(const uint16_t *p, s16x8 (&f)[1]) { f[0] = *reinterpret_cast<const s16x8 *>(p); }
-__device__ __forceinline__ void fragment(const float *p, s16x8 (&f)[3])
+template <typename Tin, int NB>
+__device__ __forceinline__ void fragment(Buffer b, unsigned at, s16x8 (&f)[NB])
 {
-    split8<3>(*reinterpret_cast<const f32x4 *>(p), *reinterpret_cast<const f32x4 *>(p + 4), f);
+    if constexpr (NB == 1)
+        f[0] = __builtin_bit_cast(s16x8, fetch4(b, at));
+    else
+        split8<NB>(__builtin_bit_cast(f32x4, fetch4(b, at)), __builtin_bit_cast(f32x4, fetch4(b, at + 16)), f);
 }
 
 // Waves per SIMD: two workgroups share a compute unit with bf16 inputs (80 KB of LDS each).
@@ -117,8 +120,10 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
         bool on = mine < live;
 
         // The rows of K or Q to LDS, in bf16 pieces; rows behind the end are 0.
-        auto stage_rows = [&](const void *src) {
-            const Tin *x = static_cast<const Tin *>(src) + qk0;
+        const unsigned qrow = static_cast<unsigned>(qs * sizeof(Tin));  // bytes of a row of q or k
+        const Buffer qb = rows_buffer(static_cast<const Tin *>(p.q) + qk0, live, qs);
+        const Buffer kb = rows_buffer(static_cast<const Tin *>(p.k) + qk0, live, qs);
+        auto stage_rows = [&](Buffer src) {
             constexpr int N = TB * (K / 8) / 256, STEP = N < 4 ? N : 4;
 #pragma unroll
             for (int i0 = 0; i0 < N; i0 += STEP) {
@@ -126,14 +131,14 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
 #pragma unroll
                 for (int i = 0; i < STEP; ++i) {
                     const int u = tid + 256 * (i0 + i), t = u / (K / 8), c = 8 * (u % (K / 8));
-                    fragment(x + min(t, live - 1) * qs + c, f[i]);
+                    fragment<Tin>(src, t * qrow + c * static_cast<unsigned>(sizeof(Tin)), f[i]);
                 }
 #pragma unroll
                 for (int i = 0; i < STEP; ++i) {
                     const int u = tid + 256 * (i0 + i), t = u / (K / 8), c = 8 * (u % (K / 8));
 #pragma unroll
                     for (int y = 0; y < NB; ++y)
-                        *reinterpret_cast<s16x8 *>(&sm.rows[y][t][c]) = t < live ? f[i][y] : s16x8{0, 0, 0, 0, 0, 0, 0, 0};
+                        *reinterpret_cast<s16x8 *>(&sm.rows[y][t][c]) = f[i][y];
                 }
             }
         };
@@ -174,7 +179,9 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
             sm.beta[lane] = beta;
         }
         const size_t v0 = (tok0 * p.H + h) * p.V, vs = static_cast<size_t>(p.H) * p.V;
-        const size_t mrow = v0 + (on ? mine : 0) * vs + 4 * quad;
+        const Buffer bo = rows_buffer(p.d_o + v0, live, vs), by = rows_buffer(p.dv + v0, live, vs);
+        const Buffer br = rows_buffer(p.resid + v0, live, vs);
+        const unsigned mrow = static_cast<unsigned>(mine * vs + 4 * quad) * 4;
         const float *sp = p.ckpt + ((static_cast<size_t>(b) * nblk + blk) * p.H + h) * K * p.V + 4 * tid;
         const float *gp = p.work + ((static_cast<size_t>(b) * nblk + blk) * p.H + h) * K * p.V + 4 * tid;
 
@@ -194,10 +201,10 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
             f32x4 s4[UNITS], g4[UNITS], x4[3][2];  // units of S and G; dO, Y, R at columns 4 quad and 16 + 4 quad
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const size_t at = mrow + v + 16 * e;
-                x4[0][e] = *reinterpret_cast<const f32x4 *>(p.d_o + at);
-                x4[1][e] = *reinterpret_cast<const f32x4 *>(p.dv + at);
-                x4[2][e] = *reinterpret_cast<const f32x4 *>(p.resid + at);
+                const unsigned at = mrow + 4 * (v + 16 * e);
+                x4[0][e] = __builtin_bit_cast(f32x4, fetch4(bo, at));
+                x4[1][e] = __builtin_bit_cast(f32x4, fetch4(by, at));
+                x4[2][e] = __builtin_bit_cast(f32x4, fetch4(br, at));
             }
 #pragma unroll
             for (int i = 0; i < UNITS; ++i) {
@@ -205,14 +212,6 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
                 g4[i] = *reinterpret_cast<const f32x4 *>(gp + static_cast<size_t>(v) * K + 1024 * i);
             }
             s16x8 fo[3], fv[3], fu[3];
-            if (live < TB)
-#pragma unroll
-                for (int x = 0; x < 3; ++x)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            x4[x][e][r] = on ? x4[x][e][r] : 0.f;
             split8<3>(x4[0][0], x4[0][1], fo);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -221,8 +220,7 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
                     db = fmaf(x4[1][e][r], x4[2][e][r], db);
                 x4[1][e] *= beta;
                 x4[2][e] *= beta;
-                if (on)
-                    *reinterpret_cast<f32x4 *>(p.dv + mrow + v + 16 * e) = x4[1][e];
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x4[1][e]), by, mrow + 4 * (v + 16 * e), 0, 0);
             }
             split8<3>(x4[1][0], x4[1][1], fv);
             split8<3>(x4[2][0], x4[2][1], fu);
@@ -329,7 +327,7 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
             dr[t] *= -gam;
             dc[t] *= pc;
         }
-        stage_rows(p.k);
+        stage_rows(kb);
         __syncthreads();
 
         // out += E (rows 16 w ..) or E^T (columns 16 w ..) times the staged rows
@@ -376,10 +374,9 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
         // W of this lane's row i: prefix sums over j, then over the rows i > j of the wave
         {
             s16x8 qf[K / 32][NB], kf[K / 32][NB];
-            const Tin *q = static_cast<const Tin *>(p.q) + qk0 + static_cast<size_t>(on ? mine : 0) * qs + 8 * quad;
 #pragma unroll
             for (int m = 0; m < K / 32; ++m) {
-                fragment(q + 32 * m, qf[m]);
+                fragment<Tin>(qb, mine * qrow + static_cast<unsigned>((32 * m + 8 * quad) * sizeof(Tin)), qf[m]);
 #pragma unroll
                 for (int x = 0; x < NB; ++x)
                     kf[m][x] = lds8(&sm.rows[x][mine][32 * m + 8 * quad]);
@@ -434,7 +431,7 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
         apply(1, false, dr);
         apply(1, true, dr);
         __syncthreads();
-        stage_rows(p.q);
+        stage_rows(qb);
         __syncthreads();
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -465,10 +462,11 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
                 p.dg[(tok0 + lane) * p.H + h] = x;
         }
         // dq, dk: the first head of a group writes, the others add
+        const Buffer dqb = rows_buffer(p.dq + qk0, live, qs), dkb = rows_buffer(p.dk + qk0, live, qs);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int t = 16 * w + 4 * quad + r;
-            float *dqr = p.dq + qk0 + min(t, live - 1) * qs + row, *dkr = p.dk + qk0 + min(t, live - 1) * qs + row;
+            const unsigned at = static_cast<unsigned>(t * qs + row) * 4;
             float x[NT], y[NT];
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
@@ -479,8 +477,8 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
                 float x0[NT], y0[NT];
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
-                    x0[i] = dqr[16 * i];
-                    y0[i] = dkr[16 * i];
+                    x0[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(dqb, at + 64 * i, 0, 0));
+                    y0[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(dkb, at + 64 * i, 0, 0));
                 }
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
@@ -488,12 +486,11 @@ __global__ __launch_bounds__(256, grad_waves<Tin>()) void gdr_grad_kernel(BwdArg
                     y[i] += y0[i];
                 }
             }
-            if (t < live)
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    dqr[16 * i] = x[i];
-                    dkr[16 * i] = y[i];
-                }
+            for (int i = 0; i < NT; ++i) {
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[i]), dqb, at + 64 * i, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y[i]), dkb, at + 64 * i, 0, 0);
+            }
         }
         __syncthreads();
     }
