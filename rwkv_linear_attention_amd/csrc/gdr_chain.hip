@@ -734,10 +734,9 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
             S[t][r] = a.first ? a.first[st0 + static_cast<size_t>(channel(t, r)) * a.V] : 0.f;
     float up = 1.f, down = 1.f;  // 2^e and 2^-e, one e for each column
     int scale_e = 0;
-    // Bring the column's scale back if an entry of S (ask = entries) or an added term asks for it.
+    // Bring the column's scale back if an entry of S or an added term (in its true size) asks for it.
     // A column's entries and terms sit in four lanes: too large in one of them, or too small in
-    // all four, is seen in the lanes' votes; maxima are formed only then.  Returns what the
-    // column was multiplied by.
+    // all four, is seen in the lanes' votes; maxima are formed only then.
     auto largest_entry = [&]() {
         float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -747,47 +746,64 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
                 top[t & 3] = fmaxf(fmaxf(fabsf(S[t][r]), fabsf(S[t][r + 1])), top[t & 3]);
         return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
     };
-    auto rescale = [&](float top, float term) -> float {
-        top = __uint_as_float(quad_max(__float_as_uint(top)));
-        term = __uint_as_float(quad_max(__float_as_uint(term)));
-        const float all = fmaxf(top, 0.125f * term);
-        const bool off = (top < 0x1p-2f && all > 0.f) || !(top <= 0x1p13f) || !(term <= 0x1p8f);
-        // to [4, 8); up stays within what its reciprocal holds
-        int e = off && all < __builtin_huge_valf() ? 3 - exponent(__float_as_uint(all)) : 0;
-        e = min(max(scale_e + e, -120), 120) - scale_e;
+    // columns in which one lane at least says yes: all sixteen?
+    auto every_column = [](bool yes) {
+        unsigned long long m = __ballot(yes);
+        m |= m >> 32;
+        m |= m >> 16;
+        return (m & 0xffffu) == 0xffffu;
+    };
+    auto column_max = [](float x) { return __uint_as_float(quad_max(__float_as_uint(x))); };
+    bool zero = false;  // the column is zero: what is added alone decides its scale
+    // asks, and so the column's new scale, depends on that column alone: results are the same
+    // whichever columns share the wave
+    auto rescale = [&](bool asks, float top, float term) {
+        int e = 0;
+        if (asks && (top > 0.f || term > 0.f) && top < __builtin_huge_valf() && term < __builtin_huge_valf()) {
+            const int of_top = top > 0.f ? exponent(__float_as_uint(top)) - scale_e : -1000;
+            const int of_term = term > 0.f ? exponent(__float_as_uint(term)) - 3 : -1000;
+            e = min(max(3 - max(of_top, of_term), -120), 120) - scale_e;  // to [4, 8)
+        }
         scale_e += e;
         up = pow2(scale_e);
         down = pow2(-scale_e);
-        const float f = ldexpf(1.f, e);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-            S[t] *= f;
-        return f;
-    };
-    auto check_entries = [&]() {
-        const float top = largest_entry();
-        unsigned long long big = __ballot(top >= 0x1p-2f);
-        big |= big >> 32;
-        big |= big >> 16;
-        if ((big & 0xffffu) != 0xffffu || __any(!(top <= 0x1p13f)))
-            rescale(top, 0.f);
-    };
-    // the terms of a chunk, about to be added
-    auto check_terms = [&](f32x4(&x)[2], f32x4(&y)[2]) {
-        float term = 0.f;
-#pragma unroll
-        for (int tau = 0; tau < 2; ++tau)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                term = fmaxf(fmaxf(fabsf(x[tau][r]), fabsf(y[tau][r])), term);
-        if (__any(!(term <= 0x1p8f))) {
-            const float f = rescale(largest_entry(), term);
+                S[t][r] = ldexpf(S[t][r], e);
+    };
+    auto check_entries = [&]() {
+        float top = largest_entry();
+        zero = false;
+        if (!every_column(top >= 0x1p-2f) || __any(!(top <= 0x1p13f))) {
+            top = column_max(top);
+            zero = top == 0.f;
+            rescale(!(top >= 0x1p-2f && top <= 0x1p13f), top, 0.f);
+        }
+    };
+    // The terms of a chunk, formed under the columns' scales and about to be added; S has decayed
+    // already.  Small ones are looked at only where the column may be smaller still: it was zero or
+    // has fallen below 1/4.
+    auto check_terms = [&](auto form, const f32x4(&x)[2], const f32x4(&y)[2], bool fell) {
+        auto largest = [&]() {
+            form();
+            float term = 0.f;
 #pragma unroll
-            for (int tau = 0; tau < 2; ++tau) {
-                x[tau] *= f;
-                if (BACK)
-                    y[tau] *= f;
-            }
+            for (int tau = 0; tau < 2; ++tau)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    term = fmaxf(fmaxf(fabsf(x[tau][r]), fabsf(y[tau][r])), term);
+            return term;
+        };
+        float term = largest();
+        const bool low = fell || zero;
+        if (__any(!(term <= 0x1p8f)) || (__any(low) && !every_column(!low || term >= 0x1p-3f))) {
+            term = column_max(term);
+            up = 1.f;  // in their true size: a scale may be 2^120 off
+            const float bare = column_max(largest());
+            rescale(!(term <= 0x1p8f) || (low && term < 0x1p-3f), column_max(largest_entry()), bare);
+            form();
         }
     };
 
@@ -827,6 +843,7 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
             store(a.rows, c * C, R);
     };
     int kslot = 0;  // s % 3
+    bool fell = false;  // the last chunk's decay was below 1/4
     for (int s = 0; s < n; ++s) {
         const int slot = s & 1, c = BACK ? n - 1 - s : s;
         const auto &kr = sm.k[kslot];
@@ -872,8 +889,9 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
         if (MODE == FWD && s > 0)
             store_rows(c - 1);
         // a chunk adds at most 2^14 (backward: twice that), which twice over still fits on top of 2^13
-        if (BACK || (s & 1) == 0)
+        if (BACK || (s & 1) == 0 || fell)
             check_entries();
+        fell = static_cast<unsigned>(__builtin_amdgcn_readfirstlane(__float_as_uint(gC))) < 0x3e800000u;
         if constexpr (!BACK && NP == 1)
 #pragma unroll
             for (int m = 0; m < NM; ++m)
@@ -942,10 +960,13 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
                 S[t] *= gC;
+            check_terms(
+                [&]() {
 #pragma unroll
-            for (int tau = 0; tau < 2; ++tau)
-                u[tau] = (con[1][tau] * up) * R[tau];
-            check_terms(u, u);
+                    for (int tau = 0; tau < 2; ++tau)
+                        u[tau] = con[1][tau] * (R[tau] * up);
+                },
+                u, u, fell);
             split8h<2>(u[0], u[1], up2, m1);
 #pragma unroll
             for (int t = 0; t < NT; t += 2) {
@@ -972,18 +993,22 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
             split8<3>(R[0], R[1], zp);
             mma2<3, 3>(R[0], R[1], tf[0], tf[1], zp);
 #pragma unroll
-            for (int tau = 0; tau < 2; ++tau) {
-                u[tau] = con[1][tau] * (R[tau] * up);
-                y[tau] = con[2][tau] * (v[tau] * up);
-            }
-            check_terms(u, y);
+            for (int t = 0; t < NT; ++t)
+                S[t] *= gC;
+            check_terms(
+                [&]() {
+#pragma unroll
+                    for (int tau = 0; tau < 2; ++tau) {
+                        u[tau] = con[1][tau] * (R[tau] * up);
+                        y[tau] = con[2][tau] * (v[tau] * up);
+                    }
+                },
+                u, y, fell);
             split8h<2>(u[0], u[1], up2, m1);
             split8h<2>(y[0], y[1], yp, m1);
 #pragma unroll
             for (int t = 0; t < NT; t += 2) {
                 s16x8 x[2][NP];
-                S[t] *= gC;
-                S[t + 1] *= gC;
                 transposed(sm.q[slot], t, x[0]);
                 transposed(sm.q[slot], t + 1, x[1]);
                 mmah2<NP, 2>(S[t], S[t + 1], x[0], x[1], yp);

@@ -224,6 +224,124 @@ def test_streams_and_graph_replays(lib):
         assert torch.equal(again[0], o)
 
 
+@pytest.mark.parametrize("scale_s,scale_v", [(1e-40, 3e4), (1e-20, 1.0), (1e25, 1.0), (1e30, 1e30), (0.0, 1e-25),
+                                             (1.0, 1e-12), (1e-6, 1e6)])
+def test_magnitudes(lib, scale_s, scale_v):
+    """The rule is linear in (state, v): any scale of either must come through the matrix cores' pieces."""
+    inp = make(2, 100, 1, 2, 64, 64, seed=21, dtype="fp32", decay=0.2)
+    inp["state"] = inp["state"] * scale_s
+    inp["v"] = inp["v"] * scale_v
+    inp["v"][:, 40:] *= 1e-3      # and a change of scale on the way
+    inp["v"][1, :, :, 32:] = 0.0  # columns that only decay
+    ref_o, ref_s, _ = gdr.forward(*(inp[n] for n in NAMES), inp["state"], 1.0)
+    d = on_gpu(inp)
+    o, s = lib.gdr_forward(*(d[n] for n in NAMES), d["state"], scale=1.0)
+    for b in range(2):     # each half of each row on its own: one may be 1e30 times the other
+        for cols in (slice(0, 32), slice(32, 64)):
+            if 0 < np.abs(ref_s[b, :, :, cols]).max() < 1e-30:   # fp32 itself has fewer bits from 1e-38 down
+                continue
+            check(s[b:b + 1, :, :, cols], ref_s[b:b + 1, :, :, cols], TOL, "state", (1,))
+            check(o[b:b + 1, :, :, cols], ref_o[b:b + 1, :, :, cols], TOL, "o", (2,))
+
+
+@pytest.mark.parametrize("how", ["reset", "late", "both"])
+def test_a_change_of_scale_at_once(lib, how):
+    """A state of 1e6 that is dropped, values that start after some chunks of zeros."""
+    inp = make(1, 200, 1, 2, 64, 64, seed=24, dtype="fp32", decay=0.2)
+    if how != "late":
+        inp["state"] = inp["state"] * 1e6
+        inp["g"][:, 70] = float("-inf")
+    if how != "reset":
+        inp["state"][:, 1] = 0
+        inp["v"][:, :90] = 0
+        inp["v"][:, 90:] *= 1e-5
+    ref_o, ref_s, _ = gdr.forward(*(inp[n] for n in NAMES), inp["state"], 1.0)
+    d = on_gpu(inp)
+    o, s = lib.gdr_forward(*(d[n] for n in NAMES), d["state"], scale=1.0)
+    check(o[:, 96:], ref_o[:, 96:], TOL, "o", (0, 2))
+    check(s, ref_s, TOL, "state", HEADS_STATE)
+
+
+@pytest.mark.parametrize("norm", [1e-4, 0.05, 1.4])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_keys_of_other_norms(lib, norm, dtype):
+    """Keys that are not normalised take the path with a power of two per row; mixed rows too."""
+    inp = make(1, 70, 1, 2, 128, 64, seed=22, dtype=dtype, key_norm=norm)
+    inp["q"] = (inp["q"].float() * 30).to(inp["q"].dtype)
+    inp["k"][0, 5] = 0
+    inp["q"][0, 33] = 0
+    ref_o, ref_s, _ = gdr.forward(*(inp[n] for n in NAMES), inp["state"], 1.0)
+    d = on_gpu(inp)
+    o, s = lib.gdr_forward(*(d[n] for n in NAMES), d["state"], scale=1.0)
+    check_o(o, ref_o, "o")
+    check(s, ref_s, TOL, "state", HEADS_STATE)
+
+
+def test_a_long_sequence(lib):
+    inp = make(1, 5000, 1, 2, 64, 64, seed=23, decay=0.05)
+    ref_o, ref_s, _ = gdr.forward(*(inp[n] for n in NAMES), inp["state"], 0.125)
+    d = on_gpu(inp)
+    o, s = lib.gdr_forward(*(d[n] for n in NAMES), d["state"])
+    check_o(o, ref_o, "o")
+    check(s, ref_s, TOL, "state", HEADS_STATE)
+
+
+def guarded(x, fill, room=4096):
+    """x inside a larger allocation filled with `fill` before and behind it."""
+    big = torch.full((x.numel() + 2 * room,), fill, dtype=x.dtype, device="cuda")
+    view = big[room:room + x.numel()].view(x.shape)
+    view.copy_(x)
+    return view, big
+
+
+@pytest.mark.parametrize("T,K,V,dtype", [(5, 128, 64, "bf16"), (33, 64, 64, "bf16"), (61, 128, 128, "fp32")])
+def test_guard_bands(lib, T, K, V, dtype):
+    """Inputs lie in NaN, outputs in a pattern: nothing beside them is used or written."""
+    inp = make(2, T, 1, 2, K, V, seed=T, dtype=dtype)
+    d = on_gpu(inp)
+    plain_o, plain_s = lib.gdr_forward(*(d[n] for n in NAMES), d["state"])
+    ins = [guarded(d[n], float("nan"))[0] for n in NAMES + ("state",)]
+    outs = {"o": torch.zeros_like(plain_o), "state_out": torch.zeros_like(plain_s)}
+    held = {n: guarded(x, -3.25) for n, x in outs.items()}
+    lengths = guarded(torch.tensor([T, T - 2], dtype=torch.int32, device="cuda"), 1 << 30)[0]
+    lib.gdr_forward(*ins, **{n: v for n, (v, _) in held.items()})
+    assert torch.equal(held["o"][0], plain_o) and torch.equal(held["state_out"][0], plain_s)
+    lib.gdr_forward(*ins, lengths=lengths, **{n: v for n, (v, _) in held.items()})
+    pos = guarded(torch.zeros(2, T, 2, K, V, device="cuda"), -3.25)
+    lib.gdr_step(*ins, state_pos=pos[0], **{n: v for n, (v, _) in held.items()})
+    for n, (v, big) in [*held.items(), ("state_pos", pos)]:
+        room = (big.numel() - v.numel()) // 2
+        assert bool((big[:room] == -3.25).all()) and bool((big[-room:] == -3.25).all()), n
+        assert not bool(v.isnan().any()), n
+
+
+def test_offsets_beyond_32_bits(lib):
+    """More than 2^32 elements in the per-position states, and in v and o of a long sequence."""
+    H, T = 8192, 66
+    inp = on_gpu(make(1, T, 1, 1, 128, 64, seed=31))
+    wide = {n: x.repeat(1, 1, *([1, 1] if n in ("q", "k") else [H] + [1] * (x.dim() - 3))) if n != "state"
+            else x.repeat(1, H, 1, 1) for n, x in inp.items()}
+    _, _, small = lib.gdr_step(*(inp[n] for n in NAMES), inp["state"], per_position=True)
+    _, _, pos = lib.gdr_step(*(wide[n] for n in NAMES), wide["state"], per_position=True)
+    assert pos.numel() > 2 ** 32
+    assert torch.equal(pos[0, :, -1], small[0, :, 0]) and torch.equal(pos[0, -1, H // 2], small[0, -1, 0])
+    del pos, wide
+    T, H = 2 ** 20 + 64, 64
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    v = torch.randn(1, T, H, 64, generator=gen, device="cuda", dtype=torch.bfloat16)
+    assert v.numel() > 2 ** 32
+    q, k = (torch.nn.functional.normalize(torch.randn(1, T, 1, 64, generator=gen, device="cuda"), dim=-1).bfloat16()
+            for _ in range(2))
+    g = -0.05 * torch.rand(1, T, H, generator=gen, device="cuda")
+    beta = torch.rand(1, T, H, generator=gen, device="cuda")
+    o, s = lib.gdr_forward(q, k, v, g, beta, o_dtype=torch.bfloat16)
+    cut = 2 ** 20       # the same from there on, from the state at the cut (a multiple of the chunk)
+    _, mid = lib.gdr_forward(*(x[:, :cut] for x in (q, k, v, g, beta)))
+    o2, s2 = lib.gdr_forward(*(x[:, cut:].contiguous() for x in (q, k, v, g, beta)), mid)
+    check(s, s2.double().cpu().numpy(), TOL, "state", HEADS_STATE)
+    check(o[:, cut:], o2.double().cpu().numpy(), TOL + BF16, "o", HEADS_SEQ, BF16)
+
+
 def test_refusals(lib):
     d = on_gpu(make(2, 12, 2, 4, 64, 64))
     args = [d[n] for n in NAMES]

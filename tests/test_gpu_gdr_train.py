@@ -27,11 +27,11 @@ def lib():
     return m
 
 
-def both(lib, inp, scale=None, d_state=True, seed=1):
+def both(lib, inp, scale=None, d_state=True, seed=1, size=1.0):
     B, T, Hk, K = inp["q"].shape
     H, V = inp["v"].shape[2:]
     gen = torch.Generator().manual_seed(seed)
-    d_o = torch.randn(B, T, H, V, generator=gen)
+    d_o = size * torch.randn(B, T, H, V, generator=gen)
     d_s = 0.3 * torch.randn(B, H, K, V, generator=gen) if d_state else None
     used = K ** -0.5 if scale is None else scale
     ref_o, ref_s, _ = gdr.forward(*(inp[n] for n in NAMES), inp["state"], used)
@@ -134,6 +134,47 @@ def test_twice_the_same_bits_and_graph_replays(lib):
         for n, x in g.items():
             assert torch.equal(x, eager[i][4][n]), n
         step(ins[1 - i])
+
+
+@pytest.mark.parametrize("size", [1e-25, 1e-9, 1e-4, 1e8])
+def test_gradients_of_any_size(lib, size):
+    """The gradients are linear in d_o: the mean over many tokens makes it small, a loss scale large."""
+    inp = make(1, 150, 1, 2, 64, 64, seed=9, dtype="fp32")
+    both(lib, inp, d_state=False, size=size)
+    both(lib, inp, size=size)    # and beside a d_state_out of its usual size
+
+
+@pytest.mark.parametrize("T,K,V,dtype", [(33, 64, 64, "bf16"), (70, 128, 64, "fp32"), (65, 128, 128, "bf16")])
+def test_guard_bands(lib, T, K, V, dtype):
+    """Inputs lie in NaN, outputs in a pattern: nothing beside them is used or written."""
+    from test_gpu_gdr import guarded
+    d = on_gpu(make(2, T, 1, 2, K, V, seed=T, dtype=dtype))
+    d["d_o"] = torch.randn(2, T, 2, V, generator=torch.Generator().manual_seed(1)).cuda()
+    names = ("o", "state_out", "ckpt", "resid")
+    fwd = dict(zip(names, lib.gdr_forward_ckpt(*(d[n] for n in NAMES), d["state"])))
+    want = lib.gdr_backward_ckpt(d["q"], d["k"], d["g"], d["beta"], fwd["ckpt"], fwd["resid"], d["d_o"], d["state"])
+    ins = {n: guarded(x, float("nan"))[0] for n, x in d.items()}
+    held = {n: guarded(torch.zeros_like(x), -3.25) for n, x in [*fwd.items(), *want.items(), ("work", fwd["ckpt"])]}
+    lib.gdr_forward_ckpt(*(ins[n] for n in NAMES), ins["state"], **{n: held[n][0] for n in names})
+    got = lib.gdr_backward_ckpt(ins["q"], ins["k"], ins["g"], ins["beta"], held["ckpt"][0], held["resid"][0],
+                                ins["d_o"], ins["state"], grads={n: held[n][0] for n in want}, work=held["work"][0])
+    for n, x in want.items():
+        assert torch.equal(got[n], x), n
+    for n, (v, big) in held.items():
+        room = (big.numel() - v.numel()) // 2
+        assert bool((big[:room] == -3.25).all()) and bool((big[-room:] == -3.25).all()), n
+
+
+def test_the_state_gradient_in_place(lib):
+    d = on_gpu(make(1, 70, 1, 2, 64, 128, seed=5))
+    o, s, ckpt, resid = lib.gdr_forward_ckpt(*(d[n] for n in NAMES), d["state"])
+    args = (d["q"], d["k"], d["g"], d["beta"], ckpt, resid, torch.ones_like(o))
+    want = lib.gdr_backward_ckpt(*args, s)
+    grads = {n: torch.empty_like(x) for n, x in want.items()}
+    grads["d_state_in"].copy_(s)
+    got = lib.gdr_backward_ckpt(*args, grads["d_state_in"], grads=grads)
+    for n, x in want.items():
+        assert torch.equal(got[n], x), n
 
 
 def test_gradients_against_differences(lib):
