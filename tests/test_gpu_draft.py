@@ -111,6 +111,31 @@ def test_one_token_with_all_the_mass(lib):
     assert sorted(set(out[:, 0].tolist())) == [0, 1093, 1094, 69999]
 
 
+@pytest.mark.parametrize("vocab,dtype", [(63, torch.float32), (4096, torch.bfloat16), (1001, torch.bfloat16)])
+def test_guard_bands_on_a_side_stream(lib, vocab, dtype):
+    """Inputs lie in ones and tokens no vocabulary holds, outputs in a pattern; the stream is the caller's."""
+    x = make(3, 4, vocab, seed=8, dtype=dtype)
+    x["u"][:] = 0.5
+    want = [t.cpu() for t in both(lib, x)]
+
+    def guarded(t, fill):
+        big = torch.full((t.numel() + 8192,), fill, dtype=t.dtype, device="cuda")
+        big[4096:4096 + t.numel()] = t.reshape(-1).cuda()
+        return big[4096:4096 + t.numel()].view(t.shape), big
+
+    ins = {n: guarded(t, 1 << 30 if t.dtype == torch.int32 else 1.0)[0] for n, t in x.items()}
+    out, kept = guarded(torch.zeros(3, 5, dtype=torch.int32), -7), guarded(torch.zeros(3, dtype=torch.int32), -7)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        lib.draft_verify(ins["target"], ins["tokens"], ins["u"], ins["u_draw"], draft=ins["draft"], out=out[0],
+                         kept=kept[0])
+    side.synchronize()
+    assert torch.equal(out[0].cpu(), want[0]) and torch.equal(kept[0].cpu(), want[1])
+    for view, big in (out, kept):
+        assert bool((big[:4096] == -7).all()) and bool((big[-4096:] == -7).all())
+
+
 def test_graph_replays(lib):
     xs = [{n: t.cuda() for n, t in make(4, 3, 5000, seed=s).items()} for s in range(3)]
     args = lambda x: (x["target"], x["tokens"], x["u"], x["u_draw"])  # noqa: E731

@@ -136,6 +136,26 @@ def test_twice_the_same_bits_and_graph_replays(lib):
         step(ins[1 - i])
 
 
+def test_two_steps_at_once_on_two_streams(lib):
+    ins = [on_gpu(make(2, 500, 2, 4, 64, 128, seed=s)) for s in range(2)]
+    d_o = torch.randn(2, 500, 4, 128, generator=torch.Generator().manual_seed(3)).cuda()
+
+    def step(d):
+        o, s, ckpt, resid = lib.gdr_forward_ckpt(*(d[n] for n in NAMES), d["state"])
+        return lib.gdr_backward_ckpt(d["q"], d["k"], d["g"], d["beta"], ckpt, resid, d_o, s)
+
+    want = [step(d) for d in ins]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ins]
+    got = []
+    for side, d in zip(streams, ins):
+        with torch.cuda.stream(side):
+            got.append(step(d))
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(a[n], b[n]) for n in a)
+
+
 @pytest.mark.parametrize("size", [1e-25, 1e-9, 1e-4, 1e8])
 def test_gradients_of_any_size(lib, size):
     """The gradients are linear in d_o: the mean over many tokens makes it small, a loss scale large."""
