@@ -12,7 +12,6 @@ using wkv7::bf16x8;
 using wkv7::f32x4;
 using wkv7::f32_to_bf16_bits;
 using wkv7::load_elem;
-using wkv7::store_elem;
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -81,7 +80,10 @@ __device__ __forceinline__ Buffer rows_buffer(T *p, int rows, size_t stride)
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(static_cast<const void *>(p)), static_cast<short>(0),
                                              static_cast<int>(bytes), 0x00027000);
 }
-__device__ __forceinline__ u32x4 fetch4(Buffer b, unsigned at) { return __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, 0); }
+__device__ __forceinline__ u32x4 fetch4(Buffer b, unsigned at)
+{
+    return __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, 0);
+}
 
 // Workgroup index to work item: consecutive workgroups go round the 8 XCDs, so each XCD
 // gets one contiguous run of items, and items that share inputs meet in its L2.

@@ -22,6 +22,10 @@
 // come straight from memory in fragment layout; U's fragments are shared through LDS.  Then
 // E1 and E2 go to LDS once (they replace the staged states) and serve as they are and
 // transposed.  Everything is on three bf16 pieces: products of magnitudes no scale is known of.
+//
+// WHAT BOUNDS IT.  2 x 4096 tokens of 32 heads of 128 x 128 on 16 key heads take 395 us for
+// 1.65 GB (S, G, dO, Y, R in, five gradients out, dq and dk twice): 4.2 TB/s, against 4.8 of a
+// plain copy.  8 x 1024 tokens of 12 heads of 64 x 64 take 67 us.
 #include <type_traits>
 
 #include "gdr_launch.h"
