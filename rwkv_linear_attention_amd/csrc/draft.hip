@@ -3,14 +3,17 @@
 // One workgroup of 16 waves per batch row.  The drafts are tested side by side (a handful of
 // gathered probabilities); then the waves sum the weights of the one vocabulary row the token
 // is drawn from -- max(p - q, 0), or p -- in 64 bits, one sum for each of 64 segments of the
-// row.  A scan over these sums (one per lane) finds the segment in which the running sum passes
-// u times the total; there every lane of wave 0 sums a run of neighbouring tokens, a second scan
-// finds the lane, and that lane walks its run.  The order of all sums is fixed.
+// row, 16 lanes a segment.  A scan over these sums (one per lane) finds the segment in which the
+// running sum passes u times the total; there every lane of wave 0 sums a run of neighbouring
+// tokens, a second scan finds the lane, and that lane walks its run.  The order of all sums is
+// fixed.
 //
-// What bounds it: one compute unit reads the two rows, 64 bytes a cycle at best (0.5 MB of a
-// 65536-token fp32 vocabulary in 3.6 us), behind a chain of four dependent memory latencies
-// (tokens, their probabilities, the row, the segment again): 13.2 us for one row of 65536 fp32
-// tokens, 16.4 us for 64 rows (33 MB, 2.0 TB/s).
+// What bounds it: the one compute unit of a row.  Its two rows (0.5 MB of a 65536-token fp32
+// vocabulary) come in at 64 bytes a cycle at best, 3.6 us, beside 64-bit sums of about as long,
+// behind a chain of four dependent memory latencies (tokens, their probabilities, the row, the
+// segment again): 10.2 us for one row, 12.4 us for 64 rows (33 MB, 2.7 TB/s).  One test for
+// infinities and NaN per 16 probabilities in the place of one for each took 13.3 us to 11.8,
+// the segment's wide loads 11.8 to 10.2.
 #include <type_traits>
 
 #include "gdr_device.h"
@@ -19,42 +22,75 @@
 namespace gdr {
 namespace {
 
-constexpr int THREADS = 1024, WAVES = THREADS / 64;
+constexpr int THREADS = 1024;  // 16 waves
 constexpr int SEGS = 64;  // segments of a vocabulary row: a lane each in the scan
 constexpr int RUN = 16;   // tokens of a lane in the last scan that are read at once
 
-// What a probability weighs: nothing unless it is a positive finite number.
-__device__ __forceinline__ float clean(float x) { return x > 0.f && x < __builtin_huge_valf() ? x : 0.f; }
+// What a probability weighs: nothing unless it is a positive finite number, whose bits are below
+// infinity's.
+constexpr uint32_t INFINITE = 0x7f800000u;
+__device__ __forceinline__ float clean(float x) { return __float_as_uint(x) < INFINITE ? x : 0.f; }
+// max(x - y, 0) in 64 bits, of such
+__device__ __forceinline__ double above(float x, float y)
+{
+    return static_cast<double>(x) - static_cast<double>(y < x ? y : x);
+}
 
 template <typename Tin>
 struct Weights {
     const Tin *p, *q;  // rows of target and draft (q may be null)
     int sure;          // the token a sure drafter holds all mass on, or -1
-    __device__ static double of(float p, float q)
+};
+
+// N consecutive elements as they are.
+template <typename Tin, int N>
+struct Unit {
+    u32x4 x;
+    __device__ __forceinline__ void zero() { x = u32x4{0, 0, 0, 0}; }
+    __device__ __forceinline__ void load(const Tin *p) { x = *reinterpret_cast<const u32x4 *>(p); }
+    __device__ __forceinline__ void clear(int e)
     {
-        const float x = clean(p), y = clean(q);
-        return x > y ? static_cast<double>(x) - static_cast<double>(y) : 0.0;
+        x[N == 4 ? e : e / 2] &= N == 4 ? 0u : e & 1 ? 0xffffu : 0xffff0000u;
     }
-    // RUN weights from x on, 0 from hi on, with all loads in flight at once
-    __device__ void some(size_t x, size_t hi, double (&y)[RUN]) const
+    __device__ __forceinline__ float at(int e) const
     {
-        float a[RUN], b[RUN];
-#pragma unroll
-        for (int e = 0; e < RUN; ++e) {
-            a[e] = b[e] = 0.f;
-            if (x + e < hi) {
-                a[e] = load_elem(p, x + e);
-                if (q)
-                    b[e] = load_elem(q, x + e);
-                else
-                    b[e] = static_cast<int>(x) + e == sure ? 1.f : 0.f;
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < RUN; ++e)
-            y[e] = of(a[e], b[e]);
+        if constexpr (N == 4)
+            return __uint_as_float(x[e]);
+        else
+            return e & 1 ? bf16_hi(x[e / 2]) : bf16_lo(x[e / 2]);
     }
 };
+template <typename Tin>
+struct Unit<Tin, 1> {
+    float x;
+    __device__ __forceinline__ void zero() { x = 0.f; }
+    __device__ __forceinline__ void load(const Tin *p) { x = load_elem(p, 0); }
+    __device__ __forceinline__ void clear(int) { x = 0.f; }
+    __device__ __forceinline__ float at(int) const { return x; }
+};
+
+// RUN weights from x on, 0 from hi on, with all loads in flight at once.
+template <typename Tin, bool WIDE>
+__device__ __forceinline__ void some(const Weights<Tin> &w, size_t x, size_t hi, double (&y)[RUN])
+{
+    constexpr int N = WIDE ? 16 / sizeof(Tin) : 1;
+    Unit<Tin, N> a[RUN / N], b[RUN / N];
+#pragma unroll
+    for (int i = 0; i < RUN / N; ++i) {
+        a[i].zero();
+        b[i].zero();
+        if (x + N * i < hi) {
+            a[i].load(w.p + x + N * i);
+            if (w.q)
+                b[i].load(w.q + x + N * i);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < RUN; ++e) {
+        const float q = !w.q && static_cast<int>(x) + e == w.sure ? 1.f : b[e / N].at(e % N);
+        y[e] = above(clean(a[e / N].at(e % N)), clean(q));
+    }
+}
 
 // Sum over the lanes up to this one.
 __device__ __forceinline__ double wave_scan(double x, int lane)
@@ -68,41 +104,60 @@ __device__ __forceinline__ double wave_scan(double x, int lane)
     return x;
 }
 
-// This lane's share of the weights of [lo, hi): units of 16 bytes where rows are aligned so.
+// This lane's share of the weights of [lo, hi), a segment that 16 lanes read: units of 16 bytes
+// where rows are aligned so.
 template <typename Tin, bool WIDE, bool PAIR>
-__device__ __forceinline__ double share(const Weights<Tin> &w, size_t lo, size_t hi, int lane)
+__device__ __forceinline__ double share(const Weights<Tin> &w, size_t lo, size_t hi, int row)
 {
     constexpr int N = WIDE ? 16 / sizeof(Tin) : 1, U = WIDE ? 16 / N : 8;  // elements of a load, loads in flight
     double sum = 0.0;
-    for (size_t base = lo; base < hi; base += 64 * N * U) {
-        float p[U][N], q[U][N];
+    for (size_t base = lo; base < hi; base += 16 * N * U) {
+        Unit<Tin, N> p[U], q[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const size_t x = base + 64 * N * u + N * lane;
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-                p[u][e] = q[u][e] = 0.f;
+            const size_t x = base + 16 * N * u + N * row;
+            p[u].zero();
+            if constexpr (PAIR)
+                q[u].zero();
             if (x < hi) {
-                if constexpr (WIDE) {
-                    load_row(w.p + x, p[u]);
-                    if constexpr (PAIR)
-                        load_row(w.q + x, q[u]);
-                } else {
-                    p[u][0] = load_elem(w.p, x);
-                    if constexpr (PAIR)
-                        q[u][0] = load_elem(w.q, x);
-                }
-                if constexpr (!PAIR)
-#pragma unroll
-                    for (int e = 0; e < N; ++e)
-                        q[u][e] = static_cast<int>(x) + e == w.sure ? 1.f : 0.f;
+                p[u].load(w.p + x);
+                if constexpr (PAIR)
+                    q[u].load(w.q + x);
             }
         }
+        if constexpr (!PAIR)
+            // the token a sure drafter holds all mass on: in one stretch of many
+            if (static_cast<size_t>(w.sure) - base < 16 * N * U)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int e = 0; e < N; ++e)
+                        if (base + 16 * N * u + N * row + e == static_cast<size_t>(w.sure)) {
+                            sum += above(clean(p[u].at(e)), 1.f);
+                            p[u].clear(e);
+                        }
+        // One test for the stretch in the place of one for each probability: the sums' vector
+        // instructions are what the kernel's time is made of.
+        uint32_t most = 0;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int e = 0; e < N; ++e)
-                sum += Weights<Tin>::of(p[u][e], q[u][e]);
+            for (int e = 0; e < N; ++e) {
+                most = max(most, __float_as_uint(p[u].at(e)));
+                if constexpr (PAIR)
+                    most = max(most, __float_as_uint(q[u].at(e)));
+            }
+        auto add = [&](auto of) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    sum += of(p[u].at(e), PAIR ? q[u].at(e) : 0.f);
+        };
+        if (most < INFINITE)
+            add([](float x, float y) { return PAIR ? above(x, y) : static_cast<double>(x); });
+        else
+            add([](float x, float y) { return above(clean(x), clean(y)); });
     }
     return sum;
 }
@@ -147,21 +202,15 @@ __global__ __launch_bounds__(THREADS) void draft_verify_kernel(DraftArgs a)
     const size_t len = ((vocab + SEGS - 1) / SEGS + 7) / 8 * 8;
     double upto, total;
     for (;;) {
-        double sum[SEGS / WAVES];
+        // a wave takes four segments, 16 lanes each
+        const int s = 4 * wave + (lane >> 4), row = lane & 15;
+        const size_t lo = min(s * len, vocab), hi = min(lo + len, vocab);
+        double sum = w.q ? share<Tin, WIDE, true>(w, lo, hi, row) : share<Tin, WIDE, false>(w, lo, hi, row);
 #pragma unroll
-        for (int i = 0; i < SEGS / WAVES; ++i) {
-            const size_t lo = min((wave + WAVES * i) * len, vocab), hi = min(lo + len, vocab);
-            sum[i] = w.q ? share<Tin, WIDE, true>(w, lo, hi, lane) : share<Tin, WIDE, false>(w, lo, hi, lane);
-        }
-#pragma unroll
-        for (int off = 32; off; off >>= 1)
-#pragma unroll
-            for (int i = 0; i < SEGS / WAVES; ++i)
-                sum[i] += __shfl_xor(sum[i], off);
-        if (lane == 0)
-#pragma unroll
-            for (int i = 0; i < SEGS / WAVES; ++i)
-                seg[wave + WAVES * i] = sum[i];
+        for (int off = 8; off; off >>= 1)
+            sum += __shfl_xor(sum, off);
+        if (row == 0)
+            seg[s] = sum;
         __syncthreads();
         upto = wave_scan(seg[lane], lane);
         total = __shfl(upto, 63);
@@ -182,11 +231,12 @@ __global__ __launch_bounds__(THREADS) void draft_verify_kernel(DraftArgs a)
         const int s = past ? __ffsll(past) - 1 : 63 - __clzll(any);
         const double before = __shfl(upto - own, s);
         // this lane's run of the segment
-        const size_t run = len / 64 + (len % 64 != 0), end = min((s + 1) * len, vocab);
+        const size_t run = WIDE ? (len + 511) / 512 * 8 : (len + 63) / 64;  // whole units
+        const size_t end = min((s + 1) * len, vocab);
         const size_t lo = min(s * len + lane * run, end), hi = min(lo + run, end);
         double y[RUN], mine = 0.0;
         for (size_t x = lo; x < hi; x += RUN) {
-            w.some(x, hi, y);
+            some<Tin, WIDE>(w, x, hi, y);
 #pragma unroll
             for (int e = 0; e < RUN; ++e)
                 mine += y[e];
@@ -200,7 +250,7 @@ __global__ __launch_bounds__(THREADS) void draft_verify_kernel(DraftArgs a)
             bool found = false;
             for (size_t i = lo; i < hi && !found; i += RUN) {
                 if (hi - lo > RUN)
-                    w.some(i, hi, y);
+                    some<Tin, WIDE>(w, i, hi, y);
 #pragma unroll
                 for (int e = 0; e < RUN; ++e) {
                     x += y[e];

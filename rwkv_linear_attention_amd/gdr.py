@@ -99,7 +99,9 @@ def _state(x, shape, device, name, new=False):
 def _output(x, shape, device, name, dtype=_f32, dtypes=F32):
     """An output argument, or a fresh tensor in the place of None."""
     if x is None:
-        x = torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
+    if torch.is_tensor(x) and x.dtype in dtypes and _good(x, shape, x.dtype, device):
+        return x
     return _out_arg(x, shape, device, name, dtypes)
 
 

@@ -49,6 +49,16 @@ def test_against_the_oracle(lib, B, N, vocab, sure, dtype):
     both(lib, make(B, N, vocab, seed=B + vocab, dtype=dtype), sure)
 
 
+@pytest.mark.parametrize("vocab,dtype", [(140008, torch.bfloat16), (200000, torch.float32), (262147, torch.bfloat16)])
+def test_runs_longer_than_one_reading(lib, vocab, dtype):
+    x = make(2, 2, vocab, seed=11, dtype=dtype)
+    for sure in (False, True):
+        both(lib, x, sure)
+    x["target"][:, :, ::7] = float("inf")   # stretches that hold what is no probability
+    x["draft"][:, :, 5::1001] = -0.0
+    both(lib, x)
+
+
 def test_row_by_row_numbers_of_drafts(lib):
     x = make(6, 3, 500, seed=2, near=0.05)
     both(lib, x, n_draft=[0, 1, 2, 3, -4, 9])
