@@ -38,7 +38,8 @@
  * their H (and 64 as N).
  *
  * NUMERICS.  The state and every accumulation are fp32.  Results match
- * an fp64 evaluation to a relative L2 error below 1e-6 (plus the rounding of a bf16 o).
+ * an fp64 evaluation to a relative L2 error below 1e-6 (plus the rounding of a bf16 o)
+ * for g <= 0; where positive g make the state grow, a few times that.
  * Value channels stay independent: a NaN or Inf in v[b,t,h,j] reaches only column j of
  * that head, from token t on, except that gdr_forward forms the outputs of 32 tokens
  * together, so there it can also reach the earlier tokens of the same 32-token chunk.

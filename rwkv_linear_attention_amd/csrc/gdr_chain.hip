@@ -851,7 +851,7 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
             store(a.rows, c * C, R);
     };
     int kslot = 0;  // s % 3
-    bool fell = false;  // the last chunk's decay was below 1/4
+    bool fell = false, again = false;  // the last chunk's decay was below 1/4; that, or above 1
     for (int s = 0; s < n; ++s) {
         const int slot = s & 1, c = BACK ? n - 1 - s : s;
         const auto &kr = sm.k[kslot];
@@ -896,10 +896,13 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
         __builtin_amdgcn_sched_barrier(0);
         if (MODE == FWD && s > 0)
             store_rows(c - 1);
-        // a chunk adds at most 2^14 (backward: twice that), which twice over still fits on top of 2^13
-        if (BACK || (s & 1) == 0 || fell)
+        // A chunk adds at most 2^14 (backward: twice that), which twice over still fits on top of
+        // 2^13 unless the chunk's "decay" was a growth.
+        if (BACK || (s & 1) == 0 || again)
             check_entries();
-        fell = static_cast<unsigned>(__builtin_amdgcn_readfirstlane(__float_as_uint(gC))) < 0x3e800000u;
+        const unsigned decay = __builtin_amdgcn_readfirstlane(__float_as_uint(gC));
+        fell = decay < 0x3e800000u;
+        again = fell || decay > 0x3f800000u;
         if constexpr (!BACK && NP == 1)
 #pragma unroll
             for (int m = 0; m < NM; ++m)

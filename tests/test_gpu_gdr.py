@@ -262,6 +262,17 @@ def test_a_change_of_scale_at_once(lib, how):
     check(s, ref_s, TOL, "state", HEADS_STATE)
 
 
+def test_states_that_grow(lib):
+    """A positive g is no decay, but nothing forbids it: 0.3 a token multiplies the state by 1e13."""
+    inp = make(1, 100, 1, 2, 64, 64, seed=25, dtype="fp32")
+    inp["g"] = inp["g"].abs().clamp(max=0.3)
+    ref_o, ref_s, _ = gdr.forward(*(inp[n] for n in NAMES), inp["state"], 1.0)
+    d = on_gpu(inp)
+    o, s = lib.gdr_forward(*(d[n] for n in NAMES), d["state"], scale=1.0)
+    check(o, ref_o, TOL, "o", HEADS_SEQ)
+    check(s, ref_s, TOL, "state", HEADS_STATE)
+
+
 @pytest.mark.parametrize("norm", [1e-4, 0.05, 1.4])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_keys_of_other_norms(lib, norm, dtype):
