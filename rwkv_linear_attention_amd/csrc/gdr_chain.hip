@@ -106,19 +106,6 @@ __device__ __forceinline__ void fetch(uint16_t &x, Buffer b, unsigned at)
 {
     x = __builtin_amdgcn_raw_buffer_load_b16(b, at, 0, 0);
 }
-// Two fp32 values to two places.
-__device__ __forceinline__ void put2(const float *, Buffer b, unsigned at0, unsigned at1, float x, float y)
-{
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), b, at0, 0, 0);
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y), b, at1, 0, 0);
-}
-__device__ __forceinline__ void put2(const uint16_t *, Buffer b, unsigned at0, unsigned at1, float x, float y)
-{
-    const uint32_t u = pk_bf16(x, y);
-    __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(u), b, at0, 0, 0);
-    __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(u >> 16), b, at1, 0, 0);
-}
-
 // Eight input elements of a row.
 template <typename Tin> struct Raw;
 template <> struct Raw<uint16_t> {
@@ -172,6 +159,16 @@ __device__ __forceinline__ int exponent(uint32_t bits)
     return bits == 0 || e == 255 ? 0 : min(max(e - 126, -120), 120);
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// Four consecutive values.
+__device__ __forceinline__ void put4(const float *, Buffer b, unsigned at, const f32x4 x)
+{
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), b, at, 0, 0);
+}
+__device__ __forceinline__ void put4(const uint16_t *, Buffer b, unsigned at, const f32x4 x)
+{
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3])}, b, at, 0, 0);
+}
 
 // What every wave of a workgroup knows.
 struct Place {
@@ -729,6 +726,9 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             at[tau][r] = static_cast<unsigned>((16 * tau + 4 * quad + r) * vs + col);
+    // and of four columns of a token
+    const unsigned turned[2] = {static_cast<unsigned>(row * vs + (col - row) + 4 * quad),
+                                static_cast<unsigned>((16 + row) * vs + (col - row) + 4 * quad)};
     const size_t st0 = static_cast<size_t>(head) * K * a.V + col;  // [b, h, 0, col] of a state
     auto channel = [&](int t, int r) { return 32 * (t >> 1) + 8 * quad + 4 * (t & 1) + r; };
     using Trow = typename std::conditional<BACK, float, Tin>::type;
@@ -741,6 +741,7 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
         for (int r = 0; r < 4; ++r)
             S[t][r] = a.first ? a.first[st0 + static_cast<size_t>(channel(t, r)) * a.V] : 0.f;
     float up = 1.f, down = 1.f;  // 2^e and 2^-e, one e for each column
+    f32x4 down4 = {1.f, 1.f, 1.f, 1.f};  // down of the columns 4 quad .. 4 quad + 3
     int scale_e = 0;
     // Bring the column's scale back if an entry of S or an added term (in its true size) asks for it.
     // A column's entries and terms sit in four lanes: too large in one of them, or too small in
@@ -775,6 +776,10 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
         scale_e += e;
         up = pow2(scale_e);
         down = pow2(-scale_e);
+        if (!BACK)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                down4[r] = __shfl(down, 4 * quad + r);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -825,30 +830,38 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
             for (int r = 0; r < 4; ++r)
                 fetch(next[tau][r], b, at[tau][r] * static_cast<unsigned>(sizeof(Trow)));
     };
-    // rows of a chunk, to out[t][col]
-    auto store = [&](auto *out, int first, const f32x4(&x)[2]) {
-        const Buffer b = rows_buffer(out + row0 + first * vs, min(L - first, C), vs);
-        constexpr unsigned size = sizeof(*out);
+    // The residuals of a chunk: a column a lane, as the products with them need it.
+    auto store_rows = [&](int first, const f32x4(&x)[2]) {
+        const Buffer b = rows_buffer(a.rows + row0 + first * vs, min(L - first, C), vs);
 #pragma unroll
         for (int tau = 0; tau < 2; ++tau)
 #pragma unroll
-            for (int r = 0; r < 4; r += 2)
-                put2(out, b, at[tau][r] * size, at[tau][r + 1] * size, x[tau][r], x[tau][r + 1]);
+            for (int r = 0; r < 4; ++r)
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[tau][r]), b, at[tau][r] * 4, 0, 0);
+    };
+    // The outputs: their products are formed transposed, a token a lane, so that four columns go
+    // in one store (8 x 4096 x 12 heads 153 -> 150 us).
+    auto store_out = [&](int first, const f32x4(&x)[2]) {
+        Tout *out = static_cast<Tout *>(a.o);
+        const Buffer b = rows_buffer(out + row0 + first * vs, min(L - first, C), vs);
+#pragma unroll
+        for (int tau = 0; tau < 2; ++tau)
+            put4(out, b, turned[tau] * static_cast<unsigned>(sizeof(Tout)), x[tau]);
     };
     if (n > 0)
         load(0);
     __syncthreads();
     __syncthreads();
     __syncthreads();
-    // A chunk's rows are stored at the top of the next: the addresses and stores then run while
-    // the first operands are on their way.  (With the checkpoints' or residuals' stores beside
-    // them that costs more than it hides: 67 against 72 us on 8 x 1024 x 12 heads.)
+    // The plain forward pass stores a chunk's outputs at the top of the next: addresses and stores
+    // then run while the first operands are on their way (8 x 4096 x 12 heads 155 -> 150 us; beside
+    // the checkpoints' and residuals' stores it gives nothing).
     f32x4 O[2], R[2];
-    auto store_rows = [&](int c) {
+    auto store_chunk = [&](int c) {
         if constexpr (MODE != BWD)
-            store(static_cast<Tout *>(a.o), c * C, O);
+            store_out(c * C, O);
         if constexpr (MODE != FWD)
-            store(a.rows, c * C, R);
+            store_rows(c * C, R);
     };
     int kslot = 0;  // s % 3
     bool fell = false, again = false;  // the last chunk's decay was below 1/4; that, or above 1
@@ -875,12 +888,17 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
         }
         // Operands are asked for well before the products that use them: a wave alone on its SIMD
         // has nothing else to hide the LDS behind.
-        f32x4 con[3][2];
+        f32x4 con[BACK ? 3 : 2][2];
+        float scaled[2];  // scale gamma and Q's row factor of this lane's tokens
 #pragma unroll
-        for (int x = 0; x < 3; ++x)
+        for (int x = 0; x < (BACK ? 3 : 2); ++x)
 #pragma unroll
             for (int tau = 0; tau < 2; ++tau)
                 con[x][tau] = *reinterpret_cast<const f32x4 *>(&sm.con[s & 3][x][16 * tau + 4 * quad]);
+        if (!BACK)
+#pragma unroll
+            for (int tau = 0; tau < 2; ++tau)
+                scaled[tau] = sm.con[s & 3][2][16 * tau + row];
         const float gC = sm.vec[s & 3][0][C - 1];
         auto rows_of = [&](const uint16_t(&x)[NP][C][K + 16], int m, s16x8(&f)[2][NP]) {
 #pragma unroll
@@ -895,7 +913,7 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
             rows_of(kr, m, kf[m]);
         __builtin_amdgcn_sched_barrier(0);
         if (MODE == FWD && s > 0)
-            store_rows(c - 1);
+            store_chunk(c - 1);
         // A chunk adds at most 2^14 (backward: twice that), which twice over still fits on top of
         // 2^13 unless the chunk's "decay" was a growth.
         if (BACK || (s & 1) == 0 || again)
@@ -939,7 +957,7 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
             for (int m = 0; m < NM; ++m) {
                 if constexpr (NP != 1)
                     rows_of(sm.q[slot], m, qf[m]);
-                mmah2<NP, 2>(qs[0], qs[1], qf[m][0], qf[m][1], Sp[m]);
+                mmah2<NP, 2, true>(qs[0], qs[1], qf[m][0], qf[m][1], Sp[m]);
             }
         // K^T or Q^T of state tile t
         auto transposed = [&](const uint16_t(&x)[NP][C][K + 16], int t, s16x8(&f)[NP]) {
@@ -951,7 +969,7 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
         f32x4 u[2];
         s16x8 zp[3], up2[2];
         if constexpr (!BACK) {
-            const float qdown = down;  // qs was formed under this scale
+            const f32x4 qdown = down4;  // qs was formed under this scale
 #pragma unroll
             for (int tau = 0; tau < 2; ++tau) {
                 const f32x4 c = con[0][tau] * down;
@@ -991,8 +1009,8 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
             split8<NA>(R[0], R[1], rp);
 #pragma unroll
             for (int tau = 0; tau < 2; ++tau)
-                O[tau] = (con[2][tau] * qdown) * qs[tau];
-            mma2<NA, NA>(O[0], O[1], af[0], af[1], rp);
+                O[tau] = (scaled[tau] * qdown) * qs[tau];
+            mma2<NA, NA, true>(O[0], O[1], af[0], af[1], rp);
         } else {
             f32x4 y[2];
             s16x8 yp[2];
@@ -1029,11 +1047,11 @@ __global__ __launch_bounds__(512) void gdr_chain_kernel(ChainArgs a)
             }
         }
         if (MODE != FWD)
-            store_rows(c);
+            store_chunk(c);
         __syncthreads();
     }
     if (MODE == FWD && n > 0)
-        store_rows(n - 1);
+        store_chunk(n - 1);
     if (n > 0 || a.first != a.last)
 #pragma unroll
         for (int t = 0; t < NT; ++t)

@@ -137,8 +137,9 @@ __device__ __forceinline__ s16x8 cat(const s16x4 a, const s16x4 b)
 }
 
 // Two accumulators at once, with the same right operand: their chains of dependent products
-// alternate.
-template <int NPA, int NPB>
+// alternate.  TURN: the products transposed (the pieces change places; both operands have the
+// same layout).
+template <int NPA, int NPB, bool TURN = false>
 __device__ __forceinline__ void mma2(f32x4 &acc0, f32x4 &acc1, const s16x8 (&A0)[NPA], const s16x8 (&A1)[NPA],
                                      const s16x8 (&B)[NPB])
 {
@@ -150,12 +151,13 @@ __device__ __forceinline__ void mma2(f32x4 &acc0, f32x4 &acc1, const s16x8 (&A0)
             const int r = s - p;
             if (r >= 0 && r < NPB) {
                 const bf16x8 b = __builtin_bit_cast(bf16x8, B[r]);
-                acc0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, A0[p]), b, acc0, 0, 0, 0);
-                acc1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, A1[p]), b, acc1, 0, 0, 0);
+                const bf16x8 a0 = __builtin_bit_cast(bf16x8, A0[p]), a1 = __builtin_bit_cast(bf16x8, A1[p]);
+                acc0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(TURN ? b : a0, TURN ? a0 : b, acc0, 0, 0, 0);
+                acc1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(TURN ? b : a1, TURN ? a1 : b, acc1, 0, 0, 0);
             }
         }
 }
-template <int NPA, int NPB>
+template <int NPA, int NPB, bool TURN = false>
 __device__ __forceinline__ void mmah2(f32x4 &acc0, f32x4 &acc1, const s16x8 (&A0)[NPA], const s16x8 (&A1)[NPA],
                                       const s16x8 (&B)[NPB])
 {
@@ -167,8 +169,9 @@ __device__ __forceinline__ void mmah2(f32x4 &acc0, f32x4 &acc1, const s16x8 (&A0
             const int r = s - p;
             if (r >= 0 && r < NPB) {
                 const f16x8 b = __builtin_bit_cast(f16x8, B[r]);
-                acc0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, A0[p]), b, acc0, 0, 0, 0);
-                acc1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, A1[p]), b, acc1, 0, 0, 0);
+                const f16x8 a0 = __builtin_bit_cast(f16x8, A0[p]), a1 = __builtin_bit_cast(f16x8, A1[p]);
+                acc0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(TURN ? b : a0, TURN ? a0 : b, acc0, 0, 0, 0);
+                acc1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(TURN ? b : a1, TURN ? a1 : b, acc1, 0, 0, 0);
             }
         }
 }
