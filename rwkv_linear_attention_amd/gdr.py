@@ -24,7 +24,7 @@ _f32 = torch.float32
 
 def _on(device):
     """The device's own context, where another device is current."""
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():
         return _SAME
     return torch.cuda.device(device)
 
