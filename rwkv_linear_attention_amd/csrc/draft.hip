@@ -11,9 +11,9 @@
 // What bounds it: the one compute unit of a row.  Its two rows (0.5 MB of a 65536-token fp32
 // vocabulary) come in at 64 bytes a cycle at best, 3.6 us, beside 64-bit sums of about as long,
 // behind a chain of four dependent memory latencies (tokens, their probabilities, the row, the
-// segment again): 10.2 us for one row, 12.4 us for 64 rows (33 MB, 2.7 TB/s).  One test for
+// segment again): 9.5 us for one row, 11.7 us for 64 rows (33 MB, 2.9 TB/s).  One test for
 // infinities and NaN per 16 probabilities in the place of one for each took 13.3 us to 11.8,
-// the segment's wide loads 11.8 to 10.2.
+// the segment's wide loads 11.8 to 10.2, scans without LDS 10.2 to 9.5.
 #include <type_traits>
 
 #include "gdr_device.h"
@@ -92,16 +92,40 @@ __device__ __forceinline__ void some(const Weights<Tin> &w, size_t x, size_t hi,
     }
 }
 
+// x moved along its row of 16 lanes by a DPP control; lanes that nothing reaches get 0.
+template <int CTRL>
+__device__ __forceinline__ double row_move(double x)
+{
+    const u32x2 u = __builtin_bit_cast(u32x2, x);
+    return __builtin_bit_cast(double, u32x2{static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, u[0], CTRL, 0xf, 0xf, true)),
+                                            static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, u[1], CTRL, 0xf, 0xf, true))});
+}
+__device__ __forceinline__ double read_lane(double x, int lane)
+{
+    const u32x2 u = __builtin_bit_cast(u32x2, x);
+    return __builtin_bit_cast(double, u32x2{static_cast<uint32_t>(__builtin_amdgcn_readlane(u[0], lane)),
+                                            static_cast<uint32_t>(__builtin_amdgcn_readlane(u[1], lane))});
+}
+
+// Sum over a row of 16 lanes, to its first.
+__device__ __forceinline__ double row_sum(double x)
+{
+    x += row_move<0x128>(x);  // row_ror:8, 4, 2, 1
+    x += row_move<0x124>(x);
+    x += row_move<0x122>(x);
+    return x + row_move<0x121>(x);
+}
+
 // Sum over the lanes up to this one.
 __device__ __forceinline__ double wave_scan(double x, int lane)
 {
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const double y = __shfl_up(x, off);
-        if (lane >= off)
-            x += y;
-    }
-    return x;
+    x += row_move<0x111>(x);  // row_shr:1, 2, 4, 8
+    x += row_move<0x112>(x);
+    x += row_move<0x114>(x);
+    x += row_move<0x118>(x);
+    // the rows before this one
+    const double first = read_lane(x, 15), second = first + read_lane(x, 31), third = second + read_lane(x, 47);
+    return x + (lane < 16 ? 0.0 : lane < 32 ? first : lane < 48 ? second : third);
 }
 
 // This lane's share of the weights of [lo, hi), a segment that 16 lanes read: units of 16 bytes
@@ -206,14 +230,12 @@ __global__ __launch_bounds__(THREADS) void draft_verify_kernel(DraftArgs a)
         const int s = 4 * wave + (lane >> 4), row = lane & 15;
         const size_t lo = min(s * len, vocab), hi = min(lo + len, vocab);
         double sum = w.q ? share<Tin, WIDE, true>(w, lo, hi, row) : share<Tin, WIDE, false>(w, lo, hi, row);
-#pragma unroll
-        for (int off = 8; off; off >>= 1)
-            sum += __shfl_xor(sum, off);
+        sum = row_sum(sum);
         if (row == 0)
             seg[s] = sum;
         __syncthreads();
         upto = wave_scan(seg[lane], lane);
-        total = __shfl(upto, 63);
+        total = read_lane(upto, 63);
         if (total > 0.0 || (!w.q && w.sure < 0))
             break;
         w.q = nullptr;  // nothing left of max(p - q, 0): p itself
@@ -229,7 +251,7 @@ __global__ __launch_bounds__(THREADS) void draft_verify_kernel(DraftArgs a)
         // the first segment whose running sum passes the mark, or the last with any weight
         unsigned long long any = __ballot(own > 0.0), past = __ballot(own > 0.0 && upto > mark);
         const int s = past ? __ffsll(past) - 1 : 63 - __clzll(any);
-        const double before = __shfl(upto - own, s);
+        const double before = read_lane(upto - own, s);
         // this lane's run of the segment
         const size_t run = WIDE ? (len + 511) / 512 * 8 : (len + 63) / 64;  // whole units
         const size_t end = min((s + 1) * len, vocab);
@@ -261,7 +283,7 @@ __global__ __launch_bounds__(THREADS) void draft_verify_kernel(DraftArgs a)
                 }
             }
         }
-        drawn = __shfl(drawn, owner);
+        drawn = __builtin_amdgcn_readlane(drawn, owner);
     }
     int *out = a.out + static_cast<size_t>(b) * (a.N + 1);
     for (int j = lane; j <= a.N; j += 64)
